@@ -36,6 +36,19 @@ class Layer(ctypes.Structure):
                 ("slot_of", P), ("scales", P), ("codebooks", P)]
 
 
+class Dense(ctypes.Structure):
+    """pmoe_dense: dense expert matrices of a prompt's grouped products (device pointers)."""
+    _fields_ = [("type", i32), ("E", i32), ("N", i32), ("K", i32), ("w", P), ("scales", P)]
+
+
+class Rows(ctypes.Structure):
+    """pmoe_rows: the input rows of a grouped product (device pointers)."""
+    _fields_ = [("type", i32), ("n", i32), ("x", P), ("scales", P), ("index", P)]
+
+
+BF16, Q8, F32 = 0, 1, 2  # pmoe_type
+
+
 class CacheStats(ctypes.Structure):
     """pmoe_cache_stats: accumulated prefix-cache counters."""
     _fields_ = [("requests", i64), ("hits", i64), ("planes_fetched", i64), ("bytes_fetched", i64),
@@ -90,6 +103,13 @@ _SIGS = {
     "pmoe_cache_sim_independent_down": ([i32, i32, i64, i64, P, P, P, P, P, ctypes.POINTER(i64)], i32),
     "pmoe_route_host": ([P, i32, i32, i32, P, P], i32),
     "pmoe_residual_norm": ([P, P, i32, i32, P, P], i32),
+    "pmoe_quantize_q8": ([P, i32, i64, i32, P, P, P], i32),
+    "pmoe_residual_norm_q8": ([P, P, P, f32, i32, i32, P, P, P, P], i32),
+    "pmoe_group_workspace_bytes": ([i32, i32, i32], sz),
+    "pmoe_group_pairs": ([P, i32, i32, i32, P, P, P, P, sz, P], i32),
+    "pmoe_grouped_matmul": ([ctypes.POINTER(Dense), ctypes.POINTER(Rows), P, i32, i32, P, P], i32),
+    "pmoe_grouped_swiglu": ([ctypes.POINTER(Dense), ctypes.POINTER(Rows), P, i32, i32, P, P, P], i32),
+    "pmoe_combine_rows": ([P, i32, P, P, i32, i32, i32, P, P], i32),
 }
 
 for _name, (_args, _res) in _SIGS.items():
@@ -122,6 +142,14 @@ def _ptr(x):
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError(f"cannot take a pointer of {type(x)}")
+
+
+def _dense_ptr(x):
+    """_ptr of a tensor or array whose elements lie one after another (views with gaps are refused:
+    the C ABI takes no strides)."""
+    if hasattr(x, "is_contiguous") and not x.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    return _ptr(x)
 
 
 def _stream(s):
@@ -319,6 +347,61 @@ def route_host(logits, T, E, k, ids, w) -> None:
 
 def residual_norm(r, y, T, H, x, stream=None) -> None:
     _check("pmoe_residual_norm", _lib.pmoe_residual_norm(_ptr(r), _ptr(y), T, H, _ptr(x), _stream(stream)))
+
+
+def quantize_q8(w, w_is_bf16, rows, K, codes, scales, stream=None) -> None:
+    """Rows of float32 or bf16 values to e4m3 codes with a power-of-two scale byte per 32 columns."""
+    _check("pmoe_quantize_q8", _lib.pmoe_quantize_q8(_dense_ptr(w), int(w_is_bf16), rows, K, _dense_ptr(codes),
+                                                     _dense_ptr(scales), _stream(stream)))
+
+
+def residual_norm_q8(r, y, gain, eps, T, H, codes, scales, x=None, stream=None) -> None:
+    """r += y (y may be None), v = r / sqrt(mean(r^2) + eps) * gain (None: ones) as q8 rows and, with x, in bf16."""
+    _check("pmoe_residual_norm_q8", _lib.pmoe_residual_norm_q8(
+        _dense_ptr(r), _dense_ptr(y), _dense_ptr(gain), eps, T, H, _dense_ptr(codes), _dense_ptr(scales),
+        _dense_ptr(x), _stream(stream)))
+
+
+def group_workspace_bytes(T, k, E) -> int:
+    return _lib.pmoe_group_workspace_bytes(T, k, E)
+
+
+def group_pairs(ids, T, k, E, offsets, row_of, token_of, ws=None, ws_bytes=0, stream=None) -> None:
+    """The routed pairs sorted by expert (stable): offsets [E+1], row_of [T*k] (-1: no expert), token_of [T*k]."""
+    _check("pmoe_group_pairs", _lib.pmoe_group_pairs(
+        _dense_ptr(ids), T, k, E, _dense_ptr(offsets), _dense_ptr(row_of), _dense_ptr(token_of), _dense_ptr(ws),
+        ws_bytes, _stream(stream)))
+
+
+def make_dense(type, w, scales, E, N, K) -> Dense:
+    """type: BF16 (scales None) or Q8. The caller keeps w and scales alive."""
+    return Dense(type, E, N, K, _dense_ptr(w), _dense_ptr(scales))
+
+
+def make_rows(type, x, scales, n, index=None) -> Rows:
+    """n rows of x; index: int32, the x row of every sorted row (None: the sorted row itself). The caller
+    keeps the tensors alive."""
+    return Rows(type, n, _dense_ptr(x), _dense_ptr(scales), _dense_ptr(index))
+
+
+def grouped_matmul(W: Dense, X: Rows, offsets, rows, out_type, out, stream=None) -> None:
+    """out_r = W_e x_r for the sorted rows r of every expert e; out_type F32 or BF16."""
+    _check("pmoe_grouped_matmul", _lib.pmoe_grouped_matmul(
+        ctypes.byref(W), ctypes.byref(X), _dense_ptr(offsets), rows, out_type, _dense_ptr(out), _stream(stream)))
+
+
+def grouped_swiglu(W: Dense, X: Rows, offsets, rows, out_type, h, h_scales=None, stream=None) -> None:
+    """h_r = silu(Wgate_e x_r) * (Wup_e x_r), W_e = [gate | up] rows; out_type BF16 or Q8 (with h_scales)."""
+    _check("pmoe_grouped_swiglu", _lib.pmoe_grouped_swiglu(
+        ctypes.byref(W), ctypes.byref(X), _dense_ptr(offsets), rows, out_type, _dense_ptr(h), _dense_ptr(h_scales),
+        _stream(stream)))
+
+
+def combine_rows(rows, rows_are_bf16, row_of, w, T, k, H, y, stream=None) -> None:
+    """y_t = sum over the slots of w * rows[row_of], in slot order (rows outside 0..T*k-1 add nothing)."""
+    _check("pmoe_combine_rows", _lib.pmoe_combine_rows(
+        _dense_ptr(rows), int(rows_are_bf16), _dense_ptr(row_of), _dense_ptr(w), T, k, H, _dense_ptr(y),
+        _stream(stream)))
 
 
 def _event(e):

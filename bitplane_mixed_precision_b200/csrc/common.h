@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/pmoe.h"
 
@@ -32,6 +33,9 @@ inline pmoe_status launch_status() { return cuda_status(cudaGetLastError()); }
 #define PMOE_CUDA(expr) PMOE_TRY(::pmoe::cuda_status(expr))
 
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// PMOE_OK if every pointer that is not null is memory of the current device (or managed memory).
+pmoe_status on_current_device(std::initializer_list<const void *> ptrs);
 
 // Gaussian helpers (host, double): own implementations, see format.cu.
 double norm_ppf(double p);

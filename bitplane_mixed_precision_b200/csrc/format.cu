@@ -15,6 +15,21 @@ thread_local int g_last_cuda_error = 0;
 
 void set_cuda_error(cudaError_t e) { g_last_cuda_error = (int)e; }
 
+pmoe_status on_current_device(std::initializer_list<const void *> ptrs)
+{
+    int dev = 0;
+    PMOE_CUDA(cudaGetDevice(&dev));
+    for (const void *p : ptrs) {
+        if (!p)
+            continue;
+        cudaPointerAttributes a;
+        PMOE_CUDA(cudaPointerGetAttributes(&a, p));
+        if (a.type != cudaMemoryTypeManaged && (a.type != cudaMemoryTypeDevice || a.device != dev))
+            return PMOE_ERR_INVALID_ARG;
+    }
+    return PMOE_OK;
+}
+
 // ---------------------------------------------------------------- Gaussian helpers
 
 static double norm_cdf(double z) { return 0.5 * std::erfc(-z / std::sqrt(2.0)); }

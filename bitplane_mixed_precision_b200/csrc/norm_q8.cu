@@ -1,0 +1,183 @@
+// Residual addition and root-mean-square norm with an output in 8 bits (q8 rows), and the plain
+// conversion of rows to q8.
+#include <cuda_bf16.h>
+
+#include "common.h"
+#include "q8.cuh"
+
+namespace pmoe {
+
+namespace {
+
+constexpr int kMaxNormThreads = 1024;
+
+__device__ __forceinline__ uint2 bf16x4(float4 v)
+{
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// One block per token, V float4 of the row per thread, held in registers between the sum of squares and
+// the output: r and y are read once and r written once. 8 neighbouring lanes hold one 32-column block.
+template <int V>
+__global__ void __launch_bounds__(kMaxNormThreads)
+    residual_norm_q8_kernel(float *__restrict__ r, const float *__restrict__ y, const float *__restrict__ gain,
+                            float eps, int H, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                            uint16_t *__restrict__ x)
+{
+    __shared__ float part[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n4 = H / 4;
+    const int64_t row = (int64_t)blockIdx.x * H;
+    float4 v[V];
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = tid + j * blockDim.x;
+        v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < n4) {
+            v[j] = *reinterpret_cast<const float4 *>(r + row + 4 * i);
+            if (y != nullptr) {
+                const float4 d = __ldg(reinterpret_cast<const float4 *>(y + row + 4 * i));
+                v[j].x += d.x;
+                v[j].y += d.y;
+                v[j].z += d.z;
+                v[j].w += d.w;
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = tid + j * blockDim.x;
+        if (y != nullptr && i < n4)
+            *reinterpret_cast<float4 *>(r + row + 4 * i) = v[j];
+        ss = fmaf(v[j].x, v[j].x, ss);
+        ss = fmaf(v[j].y, v[j].y, ss);
+        ss = fmaf(v[j].z, v[j].z, ss);
+        ss = fmaf(v[j].w, v[j].w, ss);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1)
+        ss += __shfl_xor_sync(0xffffffffu, ss, s);
+    if (lane == 0)
+        part[warp] = ss;
+    __syncthreads();
+    float all = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1)
+        all += __shfl_xor_sync(0xffffffffu, all, s);
+    const float ms = all / (float)H + eps;
+    const float inv = ms == 0.0f ? 0.0f : 1.0f / sqrtf(ms);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = tid + j * blockDim.x;
+        if (i >= n4) // H % 128 == 0: whole warps
+            break;
+        float4 o = make_float4(v[j].x * inv, v[j].y * inv, v[j].z * inv, v[j].w * inv);
+        if (gain != nullptr) {
+            const float4 g = __ldg(reinterpret_cast<const float4 *>(gain + 4 * i));
+            o = make_float4(o.x * g.x, o.y * g.y, o.z * g.z, o.w * g.w);
+        }
+        if (x != nullptr)
+            *reinterpret_cast<uint2 *>(x + row + 4 * i) = bf16x4(o);
+        if (codes != nullptr) {
+            const uint32_t byte = q8::scale_byte(q8::top_of_8_lanes(q8::top4(o.x, o.y, o.z, o.w)));
+            *reinterpret_cast<uint32_t *>(codes + row + 4 * i) = q8::codes4(o.x, o.y, o.z, o.w, byte);
+            // the warp's four scale bytes as one word
+            const uint32_t b1 = __shfl_sync(0xffffffffu, byte, 8), b2 = __shfl_sync(0xffffffffu, byte, 16),
+                           b3 = __shfl_sync(0xffffffffu, byte, 24);
+            if (lane == 0)
+                *reinterpret_cast<uint32_t *>(scales + row / 32 + i / 8) = byte | (b1 << 8) | (b2 << 16) | (b3 << 24);
+        }
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) quantize_q8_kernel(const void *__restrict__ w, int64_t n4,
+                                                          uint8_t *__restrict__ codes, uint8_t *__restrict__ scales)
+{
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x; i0 < n4; i0 += step) { // the whole block takes every step
+        const int64_t i = i0 + threadIdx.x;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < n4) {
+            if (BF16) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(w) + i);
+                o = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+            } else {
+                o = __ldg(reinterpret_cast<const float4 *>(w) + i);
+            }
+        }
+        const uint32_t byte = q8::scale_byte(q8::top_of_8_lanes(q8::top4(o.x, o.y, o.z, o.w)));
+        if (i < n4) {
+            *reinterpret_cast<uint32_t *>(codes + 4 * i) = q8::codes4(o.x, o.y, o.z, o.w, byte);
+            if ((i & 7) == 0)
+                scales[i / 8] = (uint8_t)byte;
+        }
+    }
+}
+
+} // namespace
+} // namespace pmoe
+
+using namespace pmoe;
+
+extern "C" {
+
+pmoe_status pmoe_quantize_q8(const void *w, int w_is_bf16, int64_t rows, int K, uint8_t *codes, uint8_t *scales,
+                             pmoe_stream stream)
+{
+    if (!w || !codes || !scales || rows < 0 || K <= 0 || K % 32 || !aligned(w, 16) || !aligned(codes, 4) ||
+        rows > (INT64_MAX / 8) / K)
+        return PMOE_ERR_INVALID_ARG;
+    if (rows == 0)
+        return PMOE_OK;
+    PMOE_TRY(on_current_device({w, codes, scales}));
+    const int64_t n4 = rows * K / 4;
+    const int64_t blocks = (n4 + 255) / 256;
+    const int grid = (int)(blocks < 16 * kNumSMs ? blocks : 16 * kNumSMs);
+    if (w_is_bf16)
+        quantize_q8_kernel<true><<<grid, 256, 0, (cudaStream_t)stream>>>(w, n4, codes, scales);
+    else
+        quantize_q8_kernel<false><<<grid, 256, 0, (cudaStream_t)stream>>>(w, n4, codes, scales);
+    return launch_status();
+}
+
+pmoe_status pmoe_residual_norm_q8(float *r, const float *y, const float *gain, float eps, int T, int H, uint8_t *codes,
+                                  uint8_t *scales, uint16_t *x, pmoe_stream stream)
+{
+    if (!r || T < 0 || H <= 0 || H % 128 || !(eps >= 0.0f) || (!codes != !scales) || (!codes && !x) ||
+        !aligned(r, 16) || !aligned(y, 16) || !aligned(gain, 16) || !aligned(codes, 16) || !aligned(scales, 4) ||
+        !aligned(x, 16))
+        return PMOE_ERR_INVALID_ARG;
+    if (H > 32768)
+        return PMOE_ERR_UNSUPPORTED;
+    if (T == 0)
+        return PMOE_OK;
+    PMOE_TRY(on_current_device({r, y, gain, codes, scales, x}));
+    const int n4 = H / 4;
+    int V = 1;
+    while (V < 8 && n4 > V * 256)
+        V *= 2;
+    while (n4 > V * kMaxNormThreads)
+        V *= 2;
+    const int threads = ((n4 + V - 1) / V + 31) / 32 * 32;
+    const cudaStream_t st = (cudaStream_t)stream;
+    switch (V) {
+    case 1:
+        residual_norm_q8_kernel<1><<<T, threads, 0, st>>>(r, y, gain, eps, H, codes, scales, x);
+        break;
+    case 2:
+        residual_norm_q8_kernel<2><<<T, threads, 0, st>>>(r, y, gain, eps, H, codes, scales, x);
+        break;
+    case 4:
+        residual_norm_q8_kernel<4><<<T, threads, 0, st>>>(r, y, gain, eps, H, codes, scales, x);
+        break;
+    default:
+        residual_norm_q8_kernel<8><<<T, threads, 0, st>>>(r, y, gain, eps, H, codes, scales, x);
+        break;
+    }
+    return launch_status();
+}
+
+} // extern "C"

@@ -569,6 +569,128 @@ PMOE_API pmoe_status pmoe_route_host(const float *logits, int T, int E, int k, i
  */
 PMOE_API pmoe_status pmoe_residual_norm(float *r, const float *y, int T, int H, uint16_t *x, pmoe_stream stream);
 
+/* ------------------------------------------------------------------ */
+/* Prompts: dense experts, many tokens                                 */
+/* ------------------------------------------------------------------ */
+
+/*
+ * A prompt brings thousands of tokens to a layer at once; every expert is
+ * then hit by many of them and is best held as a dense matrix. These calls
+ * carry a routed layer from the residual stream to its output:
+ *   pmoe_residual_norm_q8 -> (router) pmoe_route -> pmoe_group_pairs ->
+ *   pmoe_grouped_swiglu -> pmoe_grouped_matmul -> pmoe_combine_rows.
+ * They are not part of the PagedMoE method; the pages decode tokens only.
+ *
+ * Device pointers are used on the current device: a call whose pointers are
+ * not memory of that device returns PMOE_ERR_INVALID_ARG. Outputs must not
+ * overlap inputs unless a call says so. Every call may be captured into a
+ * graph, and calls on different streams do not disturb each other (each
+ * with its own outputs and workspace). Results do not depend on timing.
+ *
+ * "q8" rows: e4m3 codes (1 sign, 4 exponent, 3 mantissa bits; largest value
+ * 448), and for every 32 columns of a row one scale 2^e stored as the byte
+ * e + 127. e is the least whole number >= -127 with amax <= 448 * 2^e, so no
+ * value is clipped; a value v is stored as e4m3(v * 2^-e), to nearest even.
+ * A block of zeros has e = -127. A block that holds a NaN or an infinity has
+ * the scale byte 255 and codes 0x7f (all its values are NaN).
+ */
+typedef enum { PMOE_TYPE_BF16 = 0, PMOE_TYPE_Q8 = 1, PMOE_TYPE_F32 = 2 } pmoe_type;
+
+/*
+ * pmoe_quantize_q8: rows of float (or bf16 with w_is_bf16) values to q8.
+ *   w: device [rows][K], 16-byte aligned. codes: device uint8 [rows][K],
+ *   4-byte aligned. scales: device uint8 [rows][K/32]. K % 32 == 0.
+ */
+PMOE_API pmoe_status pmoe_quantize_q8(const void *w, int w_is_bf16, int64_t rows, int K, uint8_t *codes,
+                                      uint8_t *scales, pmoe_stream stream);
+
+/*
+ * pmoe_residual_norm_q8: pmoe_residual_norm with a gain and an output in 8
+ * bits. Per token t: r_t += y_t (skipped when y is NULL), then
+ *   v_t = r_t * inv_t * gain,  inv_t = 1 / sqrt(mean of r_t^2 + eps)
+ * (inv_t = 0 where that root is 0; gain NULL = ones), stored as q8 and, when
+ * x is given, also as bf16(v_t). Sums in float, in a fixed order.
+ *   r: device float [T*H] (updated). y: device float [T*H] or NULL. gain:
+ *   device float [H] or NULL. eps >= 0. codes: device uint8 [T][H], scales:
+ *   device uint8 [T][H/32] (both or neither NULL; NULL only with x). x:
+ *   device bf16 [T*H] or NULL. Pointers 16-byte aligned (scales: 4).
+ *   H % 128 == 0, H <= 32768 (else PMOE_ERR_UNSUPPORTED).
+ */
+PMOE_API pmoe_status pmoe_residual_norm_q8(float *r, const float *y, const float *gain, float eps, int T, int H,
+                                           uint8_t *codes, uint8_t *scales, uint16_t *x, pmoe_stream stream);
+
+/*
+ * pmoe_group_pairs: the routed pairs p = t*k + i sorted by expert, pairs of
+ * one expert in the order of p (a stable counting sort).
+ *   ids: device int32 [T*k] (pmoe_route's); an id outside 0..E-1 marks a pair
+ *   that no expert takes (a padded token). Ids may repeat within a token.
+ *   offsets: device int32 [E+1] out; expert e has the sorted rows
+ *   offsets[e] .. offsets[e+1]-1. row_of: device int32 [T*k] out, a pair's
+ *   sorted row, or -1. token_of: device int32 [T*k] out, a sorted row's token
+ *   t; entries from offsets[E] on are left as they were.
+ *   ws: device scratch of pmoe_group_workspace_bytes() (at most 148*E*4;
+ *   4-byte aligned; may be NULL where that is 0).
+ *   T >= 0, 1 <= k <= 32, 1 <= E <= 2048 (more: PMOE_ERR_UNSUPPORTED),
+ *   T*k <= 2^30.
+ */
+PMOE_API size_t pmoe_group_workspace_bytes(int T, int k, int E);
+PMOE_API pmoe_status pmoe_group_pairs(const int32_t *ids, int T, int k, int E, int32_t *offsets, int32_t *row_of,
+                                      int32_t *token_of, void *ws, size_t ws_bytes, pmoe_stream stream);
+
+/* Dense expert matrices W_e [N][K] (device pointers, 16-byte aligned). */
+typedef struct {
+    int type;              /* PMOE_TYPE_BF16 or PMOE_TYPE_Q8 */
+    int E, N, K;           /* E <= 2048; N % 8 == 0; K % 8 == 0 (bf16) or K % 128 == 0 (q8) */
+    const void *w;         /* bf16 or e4m3 codes, [E][N][K] */
+    const uint8_t *scales; /* q8: [E][N][K/32]; bf16: NULL */
+} pmoe_dense;
+
+/* Input rows of a grouped product (device pointers, x and scales 16-byte aligned). */
+typedef struct {
+    int type;              /* the matrices' type */
+    int n;                 /* rows of x */
+    const void *x;         /* [n][K] bf16 or e4m3 codes */
+    const uint8_t *scales; /* q8: [n][K/32]; bf16: NULL */
+    const int32_t *index;  /* sorted row r reads x row index[r]; NULL: row r itself */
+} pmoe_rows;
+
+/*
+ * pmoe_grouped_matmul: out_r = W_e x_r for the sorted rows r of every expert
+ * e, offsets[e] <= r < offsets[e+1] (device, pmoe_group_pairs's). Products
+ * of bf16 or q8 values are summed in float by the tensor cores; out is
+ * rounded once.
+ *   rows: rows of out (offsets[E] <= rows; what offsets say beyond that is
+ *   not computed). Rows that no expert has are left as they were. An index
+ *   outside 0..n-1 reads zeros; without an index, n >= rows.
+ *   out: device [rows][N], float (PMOE_TYPE_F32) or bf16 (PMOE_TYPE_BF16),
+ *   16-byte aligned.
+ */
+PMOE_API pmoe_status pmoe_grouped_matmul(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offsets, int rows,
+                                         int out_type, void *out, pmoe_stream stream);
+
+/*
+ * pmoe_grouped_swiglu: the gate and up products of every expert and their
+ * SwiGLU: with N = 2*I, rows 0..I-1 of W_e the gate and I..2I-1 the up matrix,
+ *   h_r = silu(g) * u,  g = Wgate_e x_r, u = Wup_e x_r  (silu(g) = g / (1 + exp(-g))),
+ * g, u and h in float, h rounded once. Rows and offsets as
+ * pmoe_grouped_matmul.
+ *   out_type PMOE_TYPE_BF16: h bf16 [rows][I], I % 8 == 0. PMOE_TYPE_Q8: h
+ *   e4m3 codes [rows][I] and h_scales [rows][I/32], I % 32 == 0.
+ */
+PMOE_API pmoe_status pmoe_grouped_swiglu(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offsets, int rows,
+                                         int out_type, void *h, uint8_t *h_scales, pmoe_stream stream);
+
+/*
+ * pmoe_combine_rows: y_t = sum over i of w[t*k+i] * rows[row_of[t*k+i]], in
+ * float, in slot order; a pair whose row is outside 0..T*k-1 adds nothing
+ * (its weight is not read). rows: device [T*k][H], float or bf16 with
+ * rows_are_bf16; row_of: device int32 [T*k]; w: device float [T*k]; y: device
+ * float [T*H] (overwritten). H % 8 == 0, k <= 32, T*k <= 2^30; rows
+ * and y 16-byte aligned.
+ */
+PMOE_API pmoe_status pmoe_combine_rows(const void *rows, int rows_are_bf16, const int32_t *row_of, const float *w,
+                                       int T, int k, int H, float *y, pmoe_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
