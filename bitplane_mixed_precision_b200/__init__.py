@@ -109,6 +109,7 @@ _SIGS = {
     "pmoe_group_pairs": ([P, i32, i32, i32, P, P, P, P, sz, P], i32),
     "pmoe_grouped_matmul": ([ctypes.POINTER(Dense), ctypes.POINTER(Rows), P, i32, i32, P, P], i32),
     "pmoe_grouped_swiglu": ([ctypes.POINTER(Dense), ctypes.POINTER(Rows), P, i32, i32, P, P, P], i32),
+    "pmoe_grouped_error": ([ctypes.POINTER(i32), ctypes.POINTER(i32), P], i32),
     "pmoe_combine_rows": ([P, i32, P, P, i32, i32, i32, P, P], i32),
 }
 
@@ -395,6 +396,13 @@ def grouped_swiglu(W: Dense, X: Rows, offsets, rows, out_type, h, h_scales=None,
     _check("pmoe_grouped_swiglu", _lib.pmoe_grouped_swiglu(
         ctypes.byref(W), ctypes.byref(X), _dense_ptr(offsets), rows, out_type, _dense_ptr(h), _dense_ptr(h_scales),
         _stream(stream)))
+
+
+def grouped_error(stream=None):
+    """(code, detail) of a wait that ran out in a grouped product, cleared by the call (synchronises)."""
+    code, detail = i32(0), i32(0)
+    _check("pmoe_grouped_error", _lib.pmoe_grouped_error(ctypes.byref(code), ctypes.byref(detail), _stream(stream)))
+    return code.value, detail.value
 
 
 def combine_rows(rows, rows_are_bf16, row_of, w, T, k, H, y, stream=None) -> None:

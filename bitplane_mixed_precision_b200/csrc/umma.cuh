@@ -180,5 +180,75 @@ __device__ __forceinline__ void ld16x2(uint32_t taddr, uint32_t d1, float (&v)[2
             v[d][i] = __uint_as_float(r[16 * d + i]);
 }
 
+// ---- 128-byte-swizzled K-major operands (as tiled TMA loads write them)
+
+// Rows of 128 bytes (64 bf16 or 128 8-bit k), 16-byte chunks XORed with row % 8, 8-row groups 1024 bytes
+// apart (base 1024-byte aligned): layout type 2, stride byte offset 1024. The MMAs of a row's four 32-byte K
+// slices start 0, 32, 64 and 96 bytes further on.
+__device__ __forceinline__ uint64_t smem_desc_sw128(const void *p)
+{
+    const uint32_t a = pipe::smem_u32(p);
+    return (uint64_t)((a >> 4) & 0x3fffu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+// kind::f16 with both operands bf16 (type 1 in bits 7-9 and 10-12), fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N)
+{
+    return idesc_f16(M, N) | (1u << 7) | (1u << 10);
+}
+
+// kind::mxf8f6f4 with both operands e4m3 (type 0) and power-of-two scales (bit 23) per row and 32 k; the
+// scale of K slice j of four is byte j of the scale word (bits 4-5: B, bits 29-30: A).
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int j)
+{
+    return ((uint32_t)j << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
+           ((uint32_t)j << 29);
+}
+
+// D[tmem] (+)= (A * 2^sa) * (B * 2^sb)^T, M x N x 32, e4m3 inputs, scales in tensor memory.
+__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sa_tmem, uint32_t sb_tmem, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %6, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], "
+                 "p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+
+// Scale words of 128 rows for the tensor cores: row r at byte (r % 32) * 16 + (r / 32) * 4 of a 512-byte
+// block, copied to four columns of tensor memory (repeated in each quarter of its lanes). MMAs that the same
+// thread issues later see it.
+__host__ __device__ constexpr uint32_t scale_offset(int r) { return (uint32_t)((r % 32) * 16 + (r / 32) * 4); }
+
+__device__ __forceinline__ void copy_scales(uint32_t taddr, const void *p)
+{
+    const uint32_t a = pipe::smem_u32(p);
+    const uint64_t desc = (uint64_t)((a >> 4) & 0x3fffu) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// 32 consecutive fp32 columns of this thread's lane, waited for.
+__device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32])
+{
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+
 } // namespace umma
 } // namespace pmoe

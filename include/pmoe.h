@@ -681,6 +681,14 @@ PMOE_API pmoe_status pmoe_grouped_swiglu(const pmoe_dense *W, const pmoe_rows *X
                                          int out_type, void *h, uint8_t *h_scales, pmoe_stream stream);
 
 /*
+ * pmoe_grouped_error: whether a bounded wait inside a grouped product ran out
+ * (pmoe_set_wait_limit_ns; its output is then not complete) since the last
+ * such call on the current device. Waits for the stream; *code is 0 or 3,
+ * detail (may be NULL) names the wait; the record is cleared.
+ */
+PMOE_API pmoe_status pmoe_grouped_error(int *code, int *detail, pmoe_stream stream);
+
+/*
  * pmoe_combine_rows: y_t = sum over i of w[t*k+i] * rows[row_of[t*k+i]], in
  * float, in slot order; a pair whose row is outside 0..T*k-1 adds nothing
  * (its weight is not read). rows: device [T*k][H], float or bf16 with

@@ -422,3 +422,58 @@ def test_pointers_that_are_not_device_memory_are_refused(pm):
     assert ei.value.code == 1
     with pytest.raises(ValueError):
         pm.residual_norm_q8(randn(gen(1), 2, 256)[:, :128], None, None, 0.0, 2, 128, codes.cuda(), scales.cuda())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("what", ["f32", "bf16", "swiglu q8", "swiglu bf16"])
+@pytest.mark.parametrize("K,N", [(256, 1088), (1152, 576)])
+def test_grouped_products_with_many_tiles_per_sm(pm, kind, what, K, N):
+    """Enough row tiles for the wide weight tiles, several for every SM, with ragged last columns: both
+    accumulators in turn, the columns that they share, stages that wrap."""
+    rng = np.random.default_rng(K + N)
+    c = [int(n) for n in rng.integers(0, 200, 150)]
+    c[3], c[77] = 1300, 0
+    M = sum(c)
+    W, X, n, index, x64, w64 = case(kind, c, K, N, 999, seed=8)
+    p, d = products(x64, w64, c)
+    off = offsets_of(c)
+    if what in ("f32", "bf16"):
+        o = empty(M, N, dtype=torch.float32 if what == "f32" else torch.bfloat16)
+        run_matmul(pm, kind, W, X, n, index, off, M, N, K, pm.F32 if what == "f32" else pm.BF16, o)
+        torch.cuda.synchronize()
+        check_near(o, p, d, U if what == "f32" else 2.0 ** -8)
+        return
+    I = N // 2
+    v, dv = swiglu(p, d)
+    h = empty(M, I, dtype=torch.uint8 if what == "swiglu q8" else torch.bfloat16)
+    hs = empty(M, I // 32) if what == "swiglu q8" else None
+    run_swiglu(pm, kind, W, X, n, index, off, M, I, K, pm.Q8 if hs is not None else pm.BF16, h, hs)
+    torch.cuda.synchronize()
+    if hs is not None:
+        check_q8(h, hs, v, dv)
+    else:
+        check_near(h, v, dv, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+def test_grouped_wait_that_runs_out_is_reported_and_the_next_call_is_exact(pm, kind):
+    """With the wait limit at 1 ns the roles give up, after what they issued has landed; the record names
+    it, and the next call with the default limit is the same as before, bit for bit."""
+    c, K, N = [300, 0, 200, 700], 4096, 512
+    W, X, n, index, x64, w64 = case(kind, c, K, N, 64, seed=9)
+    M, off = sum(c), offsets_of(c)
+    outs = [torch.full((M, N), float("nan"), device="cuda") for _ in range(3)]
+    assert pm.grouped_error() == (0, 0)
+    run_matmul(pm, kind, W, X, n, index, off, M, N, K, pm.F32, outs[0])
+    assert pm.grouped_error() == (0, 0)
+    pm.set_wait_limit_ns(1)
+    try:
+        run_matmul(pm, kind, W, X, n, index, off, M, N, K, pm.F32, outs[1])
+        torch.cuda.synchronize()
+    finally:
+        pm.set_wait_limit_ns(0)
+    assert pm.grouped_error()[0] == 3
+    assert pm.grouped_error() == (0, 0)  # read once
+    run_matmul(pm, kind, W, X, n, index, off, M, N, K, pm.F32, outs[2])
+    assert pm.grouped_error() == (0, 0)
+    assert torch.equal(outs[0], outs[2])
