@@ -5,10 +5,12 @@
 // where 256 would leave SMs without a tile). A persistent CTA per SM takes tiles blockIdx, blockIdx + grid,
 // ...: every role finds a tile's expert in a prefix table of row tiles that the CTA makes from `offsets` when
 // it starts. Roles, one warp each unless said otherwise:
-//   - producer: tiled TMA loads of 128 bytes of k per row into a ring of stages. Input rows come by gather
-//     through the index (four rows per load, rows that no expert has are not loaded), weight rows by two
-//     boxes (for SwiGLU: the gate rows and the up rows of the same 128 columns of h, so that one thread has
-//     both for its row);
+//   - producer: tiled TMA loads of 128 bytes of k per row into a ring of stages. Weight rows come by two boxes
+//     (for SwiGLU: the gate rows and the up rows of the same 128 columns of h, so that one thread has both for
+//     its row), input rows that follow one another by boxes of 32;
+//   - four warps gather the input rows of an index with 16-byte asynchronous copies, 8 lanes a row, in the
+//     layout that TMA writes. (Gathering TMA loads of four rows were tried first: 32 of them per stage took
+//     about 2700 cycles to issue, five times the MMAs of a q8 stage.) Rows that no expert has are not loaded;
 //   - q8: two warps bring the scale bytes (one word per row and stage) into the order the tensor cores take;
 //   - MMA: one thread; four K slices per stage, accumulators in tensor memory. bf16 has two accumulators of
 //     NT columns. q8 needs tensor memory for scales too, so its two accumulators of 256 share 32 columns:
@@ -35,7 +37,8 @@ namespace {
 constexpr int kMaxDenseExperts = 2048;
 constexpr int kRows = 128;      // rows of a tile
 constexpr int kRowBytes = 128;  // bytes of k per row and stage
-constexpr int kThreads = 256;   // producer, MMA, two scale warps, four epilogue warps
+constexpr int kGatherWarps = 4;
+constexpr int kThreads = 256 + 32 * kGatherWarps; // producer, MMA, two scale warps, epilogue (4), gather (4)
 constexpr int kStageRowBytes = 128; // epilogue staging: bytes per row
 constexpr uint64_t kDrainNs = 1000ull * 1000 * 1000;
 
@@ -44,7 +47,7 @@ __device__ int g_grouped_error[2];
 
 struct Grouped {
     int E, N, K, n, rows, width, iters, ntiles; // width: output columns; iters: stages per tile
-    const uint8_t *ws, *xs;
+    const uint8_t *x, *ws, *xs;
     const int32_t *index, *offsets;
     void *out;
     uint8_t *out_scales;
@@ -64,19 +67,19 @@ template <bool Q8IN, int NT> struct Shape {
     static constexpr int kStageAt = kStages * (kA + kB);
     static constexpr int kStagingAt = kStageAt + kStages * kScales;
     static constexpr int kBarAt = kStagingAt + 4 * 32 * kStageRowBytes;
-    static constexpr int kTableAt = kBarAt + 256;
+    static constexpr int kTableAt = kBarAt + 512;
     static constexpr size_t smem(int E) { return (size_t)kTableAt + 4 * (E + 1) + 1024; } // 1024: alignment
 };
 static_assert(Shape<true, 256>::smem(kMaxDenseExperts) <= 227 * 1024, "shared memory");
 static_assert(Shape<true, 128>::smem(kMaxDenseExperts) <= 227 * 1024, "shared memory");
 
 struct Bars {
-    uint64_t full[6], scales[6], empty[6], acc_full[2], acc_free[2], done;
+    uint64_t full[6], gathered[6], scales[6], empty[6], acc_full[2], acc_free[2], done;
     uint32_t tmem;
     int abort;
     int part[kThreads / 32];
 };
-static_assert(sizeof(Bars) <= 256, "barriers");
+static_assert(sizeof(Bars) <= 512, "barriers");
 
 // A wait that gives up after limit_ns, or as soon as another role has given up.
 struct Waiter {
@@ -183,6 +186,23 @@ __device__ void row_tiles(const Grouped &g, int *first, int *part)
     __syncthreads();
 }
 
+// 16 bytes to shared memory, the first `bytes` of them (16 or 0) from src and the rest zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// An arrival once all of this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(pipe::smem_u32(bar)) : "memory");
+}
+
+// With the fast exponential and quotient (2 + |g| and 2 units in the last place of a float): far below the
+// rounding of h, and free of branches, so that a thread's 32 columns overlap. (expf and the exact quotient
+// made the epilogue of a 2048-deep q8 tile twice as long as its products.)
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
 __device__ __forceinline__ uint32_t bf16x2(float a, float b)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -206,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             pipe::mbar_init(&bars->full[s], 1);
+            pipe::mbar_init(&bars->gathered[s], 32 * kGatherWarps);
             pipe::mbar_init(&bars->scales[s], 2);
             pipe::mbar_init(&bars->empty[s], 1);
         }
@@ -235,18 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
             const Tile T = tile_at(g, first, t, kCols);
-            int4 src = make_int4(g.n, g.n, g.n, g.n); // row n: outside, reads zeros
-            const int loads = g.index ? (T.rows + 3) / 4 : (T.rows + 31) / 32;
-            if (g.index) {
-                int *s = &src.x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * lane + j < T.rows) {
-                        const int i = __ldg(g.index + T.row0 + 4 * lane + j);
-                        s[j] = (uint32_t)i < (uint32_t)g.n ? i : g.n;
-                    }
-            }
-            const uint32_t bytes = (uint32_t)(loads * (g.index ? 4 : 32) * kRowBytes + S::kB);
+            const int loads = g.index ? 0 : (T.rows + 31) / 32;
+            const uint32_t bytes = (uint32_t)(loads * 32 * kRowBytes + S::kB);
             const int second = SWIGLU ? g.width + T.col0 : T.col0 + NT / 2;
             for (int i = 0; i < g.iters; ++i, ++it) {
                 const int s = it % S::kStages, u = it / S::kStages;
@@ -260,12 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane < 2)
                     tma::load_3d(b + lane * (NT / 2) * kRowBytes, &wmap, x, lane ? second : T.col0, T.e,
                                  &bars->full[s]);
-                if (lane < loads) {
-                    if (g.index)
-                        tma::gather4(a + lane * 4 * kRowBytes, &xmap, x, src, &bars->full[s]);
-                    else
-                        tma::load_2d(a + lane * 32 * kRowBytes, &xmap, x, T.row0 + 32 * lane, &bars->full[s]);
-                }
+                if (lane < loads)
+                    tma::load_2d(a + lane * 32 * kRowBytes, &xmap, x, T.row0 + 32 * lane, &bars->full[s]);
                 __syncwarp();
             }
         }
@@ -289,10 +296,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (int k = 0; k < g.iters; ++k, ++it) {
                     const int s = it % S::kStages, u = it / S::kStages;
-                    if (!wait(&bars->full[s], u & 1, 3) || (Q8IN && !wait(&bars->scales[s], u & 1, 4))) {
+                    if (!wait(&bars->full[s], u & 1, 3) || (Q8IN && !wait(&bars->scales[s], u & 1, 4)) ||
+                        (g.index && !wait(&bars->gathered[s], u & 1, 8))) {
                         ok = false;
                         break;
                     }
+                    if (Q8IN || g.index) // what other threads stored is seen by the tensor cores from here on
+                        umma::fence_smem_async();
                     umma::fence_after_sync();
                     const uint8_t *a = smem + s * (S::kA + S::kB), *b = a + S::kA;
                     const uint64_t ad = umma::smem_desc_sw128(a), bd = umma::smem_desc_sw128(b);
@@ -420,7 +430,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4 *>(sc + 512 * (j / 4)) =
                             make_uint4(word(now[j]), word(now[j + 1]), word(now[j + 2]), word(now[j + 3]));
                     }
-                    umma::fence_smem_async();
                     __syncwarp();
                     if (lane == 0)
                         pipe::mbar_arrive(&bars->scales[s]);
@@ -428,6 +437,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         scaled:
+            __syncwarp();
+        }
+    } else if (warp >= 8) {
+        // ---- gathered input rows: a thread has one 16-byte chunk of rows r0, r0 + 16, ...
+        if (g.index) {
+            const int r0 = (warp - 8) * 4 + lane / 8, chunk = lane & 7;
+            const int64_t pitch = (int64_t)g.K * kElem;
+            const uint32_t at = (uint32_t)(r0 * kRowBytes + ((chunk ^ (r0 & 7)) << 4)); // 16 more rows: 2 KB more
+            int it = 0;
+            for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+                const Tile T = tile_at(g, first, t, kCols);
+                const uint8_t *src[kRows / 16];
+#pragma unroll
+                for (int j = 0; j < kRows / 16; ++j) {
+                    const int r = r0 + 16 * j;
+                    src[j] = nullptr;
+                    if (r < T.rows) {
+                        const int i = __ldg(g.index + T.row0 + r);
+                        if ((uint32_t)i < (uint32_t)g.n)
+                            src[j] = g.x + i * pitch + 16 * chunk;
+                    }
+                }
+                for (int i = 0; i < g.iters; ++i, ++it) {
+                    const int s = it % S::kStages, u = it / S::kStages;
+                    if (u > 0 && !warp_wait(wait, &bars->empty[s], (u - 1) & 1, 9))
+                        goto gathered;
+                    const uint32_t dst = pipe::smem_u32(smem + s * (S::kA + S::kB)) + at;
+                    const bool in = i * kRowBytes + 16 * chunk < pitch;
+#pragma unroll
+                    for (int j = 0; j < kRows / 16; ++j)
+                        if (r0 + 16 * j < T.rows) // rows outside x, and k behind K, are filled with zeros
+                            copy16(dst + j * 16 * kRowBytes, src[j] && in ? src[j] + i * kRowBytes : g.x,
+                                   src[j] && in ? 16 : 0);
+                    copies_arrive(&bars->gathered[s]);
+                }
+            }
+        gathered:
+            asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
         }
     } else {
@@ -469,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (SWIGLU) {
 #pragma unroll
                     for (int x = 0; x < 32; ++x)
-                        v[x] = v[x] / (1.0f + expf(-v[x])) * w[x];
+                        v[x] = silu(v[x]) * w[x];
                 }
                 const int base = (c % kPer) * kUnits;
                 if (OUT == PMOE_TYPE_F32) {
@@ -601,13 +648,13 @@ pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offs
     // no input rows at all: every index is outside, the map's one row is never read
     const void *x = X->n ? X->x : W->w;
     const uint64_t xd[2] = {K, (uint64_t)(X->n ? X->n : 1)}, xstride[1] = {K * elem};
-    const uint32_t xbox[2] = {(uint32_t)(kRowBytes / elem), X->index ? 1u : 32u};
+    const uint32_t xbox[2] = {(uint32_t)(kRowBytes / elem), 32u};
     PMOE_TRY(tma::make_map(&xmap, elem, 2, x, xd, xstride, xbox));
     const uint64_t wd[3] = {K, (uint64_t)W->N, (uint64_t)W->E}, wstride[2] = {K * elem, K * elem * W->N};
     const uint32_t wbox[3] = {(uint32_t)(kRowBytes / elem), narrow ? 64u : 128u, 1u};
     PMOE_TRY(tma::make_map(&wmap, elem, 3, W->w, wd, wstride, wbox));
     const Grouped g{W->E,      W->N,     W->K,      X->n,    rows, width,      (int)((K * elem + kRowBytes - 1) / kRowBytes),
-                    ntiles,    W->scales, X->scales, X->index, offsets, out, out_scales,
+                    ntiles, static_cast<const uint8_t *>(x), W->scales, X->scales, X->index, offsets, out, out_scales,
                     wait_limit_ns()};
     const int64_t tiles = most * ntiles;
     const cudaStream_t st = (cudaStream_t)stream;

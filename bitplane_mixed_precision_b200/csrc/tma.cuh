@@ -56,14 +56,5 @@ __device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, int x
                  : "memory");
 }
 
-// Four rows of a 2-D map whose box is one row high, to consecutive rows of shared memory.
-__device__ __forceinline__ void gather4(void *dst, const CUtensorMap *map, int x, int4 rows, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, "
-                 "{%2, %3, %4, %5, %6}], [%7];" ::"r"(pipe::smem_u32(dst)),
-                 "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(pipe::smem_u32(bar))
-                 : "memory");
-}
-
 } // namespace tma
 } // namespace pmoe
