@@ -1,23 +1,33 @@
 // Matrix products grouped by expert, with ragged numbers of rows: out_r = W_e x_r for the rows r of every
 // expert e, and the gate/up pair of them with SwiGLU, on the tcgen05 tensor cores.
 //
-// A tile is up to 128 rows of one expert (the MMA's M) by NT rows of its matrix (the MMA's N: 256, or 128
-// where 256 would leave SMs without a tile). A persistent CTA per SM takes tiles blockIdx, blockIdx + grid,
-// ...: every role finds a tile's expert in a prefix table of row tiles that the CTA makes from `offsets` when
-// it starts. Roles, one warp each unless said otherwise:
-//   - producer: tiled TMA loads of 128 bytes of k per row into a ring of stages. Weight rows come by two boxes
-//     (for SwiGLU: the gate rows and the up rows of the same 128 columns of h, so that one thread has both for
-//     its row), input rows that follow one another by boxes of 32;
-//   - four warps gather the input rows of an index with 16-byte asynchronous copies, 8 lanes a row, in the
-//     layout that TMA writes. (Gathering TMA loads of four rows were tried first: 32 of them per stage took
-//     about 2700 cycles to issue, five times the MMAs of a q8 stage.) Rows that no expert has are not loaded;
-//   - q8: two warps bring the scale bytes (one word per row and stage) into the order the tensor cores take;
-//   - MMA: one thread; four K slices per stage, accumulators in tensor memory. bf16 has two accumulators of
-//     NT columns. q8 needs tensor memory for scales too, so its two accumulators of 256 share 32 columns:
-//     the next tile starts once the epilogue has read those, which it does first;
+// A tile is up to ROWS rows of one expert (the MMA's M: 128 tensor-memory lanes) by NT rows of its matrix (the
+// MMA's N). An MMA takes about 128 cycles for its 4 KB of A however small N is, so the matrix rows are N: 256 of
+// them (128 where 256 would leave SMs idle) stream through at full rate whether an expert has 1 row or 128. (The
+// other way round, with N following the number of rows, cost 20 to 50 % more at 40 and 320 rows an expert, and
+// bound single rows by the MMAs.) For SwiGLU the NT rows alternate between 32 gate rows and the up rows of the same
+// columns of h, so that one thread has both.
+// An SM takes in about 64 bytes per cycle, which bounds a 128 x 256 tile at 768 cycles per stage against 512 of
+// MMAs. With many rows per expert two neighbouring SMs (PAIR) therefore share a tile of 256 x 256: each brings its
+// 128 rows of x and half of the matrix rows, the MMAs that the first one's thread issues multiply in both, and each
+// has the accumulators of its own rows.
+// A persistent CTA (or pair) takes tiles at a stride of all of them: every role finds a tile's expert in a prefix
+// table of row tiles that the CTA makes from `offsets` when it starts. Roles, one warp each unless said otherwise:
+//   - producer: tiled TMA loads of 128 bytes of k per row into a ring of stages: the matrix rows
+//     and rows of x that follow one another by few and large boxes (the SM's TMA unit is busy for 85 cycles or more
+//     per instruction, whatever its size);
+//   - four warps gather the rows of x of an index with 16-byte asynchronous copies, 8 lanes a row, in the layout
+//     that TMA writes. (Gathering TMA loads of four rows were tried first: 32 of them per stage took about 2700
+//     cycles to issue, five times the MMAs of a stage.) Rows that no expert has are not loaded;
+//   - q8: two warps bring the scale bytes (one word per row and stage) into the order the tensor cores take, loaded
+//     several stages ahead;
+//   - MMA: one thread, which waits for one barrier per stage (a second wait and a fence of its own per stage cost
+//     the q8 products 10 to 20 %: everybody else fences and arrives on that one barrier); four K slices per stage, accumulators in tensor memory: two of NT columns. q8 needs tensor
+//     memory for scales too, so its two of 256 share 64 columns: the next tile starts once the epilogue has read
+//     those, which it does first;
 //   - epilogue, four warps (one per quarter of the tensor-memory lanes = 32 rows): SwiGLU and the rounding on
-//     registers (a thread has 32 neighbouring columns of one row: a whole q8 block), then through shared
-//     memory so that rows are stored in pieces of 128 bytes.
+//     registers (a thread has 32 neighbouring columns of one row: a whole q8 block), then through shared memory so
+//     that rows are stored in pieces of 128 bytes.
 // Every wait is bounded; a wait that runs out is recorded (pmoe_grouped_error) and the CTA's roles finish in
 // turn, after their copies and MMAs in flight have landed.
 #include <cuda_bf16.h>
@@ -35,14 +45,15 @@ namespace pmoe {
 namespace {
 
 constexpr int kMaxDenseExperts = 2048;
-constexpr int kRows = 128;      // rows of a tile
-constexpr int kRowBytes = 128;  // bytes of k per row and stage
+constexpr int kRowBytes = 128; // bytes of k per row and stage
 constexpr int kGatherWarps = 4;
 constexpr int kThreads = 256 + 32 * kGatherWarps; // producer, MMA, two scale warps, epilogue (4), gather (4)
-constexpr int kStageRowBytes = 128; // epilogue staging: bytes per row
+constexpr int kLanes = 128;                       // the MMA's M
+constexpr int kStageRowBytes = 128;               // epilogue staging: bytes per row
 constexpr uint64_t kDrainNs = 1000ull * 1000 * 1000;
+constexpr uint64_t kSettleNs = 5ull * 1000 * 1000; // hundreds of times what a load takes
 
-// code of the first wait that ran out in any grouped product since pmoe_grouped_error last read it
+// the first wait that ran out in any grouped product since pmoe_grouped_error last read it: code 3 and which
 __device__ int g_grouped_error[2];
 
 struct Grouped {
@@ -54,32 +65,76 @@ struct Grouped {
     uint64_t limit_ns;
 };
 
-template <bool Q8IN, int NT> struct Shape {
-    static constexpr int kA = kRows * kRowBytes, kB = NT * kRowBytes;
-    static constexpr int kScales = Q8IN ? (kRows + NT) * 4 : 0;
-    static constexpr int kStages = NT == 256 ? 4 : 6;
-    // tensor memory: two accumulators; q8 with 256 columns: the second starts 32 columns early
+constexpr int kMostStages = 12;
+template <bool Q8IN, bool PAIR, int ROWS, int NT> struct Shape {
+    static_assert(!PAIR || (ROWS == 128 && NT == 256), "shapes");
+    static constexpr bool kPair = PAIR;
+    static constexpr int kBRows = PAIR ? NT / 2 : NT; // matrix rows in this CTA's stages
+    static constexpr int kA = ROWS * kRowBytes, kB = kBRows * kRowBytes;
+    static constexpr int kAtoms = NT / 128; // scale blocks of 128 matrix rows (a pair's CTAs have all of them)
+    static constexpr int kScales = Q8IN ? 512 * (1 + kAtoms) : 0;
+    static constexpr int kStaging = 4 * 32 * kStageRowBytes;
+    // the MMA reads 128 rows from a stage's rows of x even when it has 32 (the lanes of the others are not used):
+    // what follows has to be there
+    static constexpr int kPad = (kLanes - ROWS) * kRowBytes > kB ? (kLanes - ROWS) * kRowBytes - kB : 0;
+    static constexpr int kRoom = 227 * 1024 - 1024 - 1024 - 4 * (kMaxDenseExperts + 1) - kStaging - kPad;
+    static constexpr int kFit = kRoom / (kA + kB + kScales);
+    static constexpr int kStages = kFit < kMostStages ? kFit : kMostStages;
+    // tensor memory: two accumulators; q8 with 256 columns: the second starts 64 columns early, which leaves room
+    // for the scales of five stages
     static constexpr bool kOverlap = Q8IN && NT == 256;
-    static constexpr int kSecond = kOverlap ? NT - 32 : NT;
-    static constexpr int kScaleCols = kSecond + NT; // then two sets of scale columns
-    static constexpr int kTmemCols = kScaleCols + (Q8IN ? 32 : 0) <= 256 ? 256 : 512;
-    static_assert(kScaleCols + (Q8IN ? 32 : 0) <= 512, "tensor memory");
-    static constexpr int kStageAt = kStages * (kA + kB);
-    static constexpr int kStagingAt = kStageAt + kStages * kScales;
-    static constexpr int kBarAt = kStagingAt + 4 * 32 * kStageRowBytes;
-    static constexpr int kTableAt = kBarAt + 512;
+    static constexpr int kShared = kOverlap ? 64 : 0;
+    static constexpr int kSecond = NT - kShared;
+    static constexpr int kScaleCols = kSecond + NT; // then the sets of scale columns
+    static constexpr int kSets = kStages, kSetCols = 4 + 4 * kAtoms; // a set for each stage
+    static constexpr int kTmemUsed = kScaleCols + (Q8IN ? kSets * kSetCols : 0);
+    static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
+    static_assert(kTmemUsed <= 512, "tensor memory");
+    static_assert(kStages >= 4, "stages");
+    static constexpr int kScalesAt = kStages * (kA + kB) + kPad;
+    static constexpr int kStagingAt = kScalesAt + kStages * kScales;
+    static constexpr int kBarAt = kStagingAt + kStaging;
+    static constexpr int kTableAt = kBarAt + 1024;
     static constexpr size_t smem(int E) { return (size_t)kTableAt + 4 * (E + 1) + 1024; } // 1024: alignment
+    static_assert(kTableAt + 4 * (kMaxDenseExperts + 1) + 1024 <= 227 * 1024, "shared memory");
 };
-static_assert(Shape<true, 256>::smem(kMaxDenseExperts) <= 227 * 1024, "shared memory");
-static_assert(Shape<true, 128>::smem(kMaxDenseExperts) <= 227 * 1024, "shared memory");
 
 struct Bars {
-    uint64_t full[6], gathered[6], scales[6], empty[6], acc_full[2], acc_free[2], done;
+    uint64_t full[kMostStages]; // a stage is complete (of a pair: in both CTAs, on the first one's barrier)
+    uint64_t empty[kMostStages];
+    uint64_t acc_full[2], acc_free[2], done;
     uint32_t tmem;
     int abort;
     int part[kThreads / 32];
 };
-static_assert(sizeof(Bars) <= 512, "barriers");
+static_assert(sizeof(Bars) <= 1024, "barriers");
+
+// ---- the other CTA of a pair
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The same place in the cluster's first CTA.
+__device__ __forceinline__ uint32_t in_first(const void *p)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(pipe::smem_u32(p)));
+    return a;
+}
+
+__device__ __forceinline__ void arrive_in_first(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+}
 
 // A wait that gives up after limit_ns, or as soon as another role has given up.
 struct Waiter {
@@ -121,7 +176,31 @@ __device__ void drain(uint64_t *bar, uint32_t parity)
     }
 }
 
-// One tile: its expert, rows and first matrix row (or h column).
+__device__ __forceinline__ uint32_t bf16x2(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// The ring's stages in order: stage s for the (phase)th time.
+template <int STAGES> struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++s == STAGES) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    // whether the MMAs that read the stage before have finished; at once the first time round
+    __device__ __forceinline__ bool free(const Waiter &wait, Bars *bars, int where) const
+    {
+        return warp_wait(wait, &bars->empty[s], phase ^ 1, where);
+    }
+};
+
+// One tile: its expert, rows of x (sorted rows row0 .. row0 + rows - 1) and first output column.
 struct Tile {
     int e, row0, rows, col0;
 };
@@ -133,28 +212,40 @@ __device__ __forceinline__ int2 expert_rows(const Grouped &g, int e)
     return make_int2(a, max(a, b));
 }
 
-__device__ __forceinline__ Tile tile_at(const Grouped &g, const int *first, int t, int cols)
-{
-    const int m = t / g.ntiles;
-    int lo = 0, hi = g.E; // first[lo] <= m < first[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (first[mid] <= m)
-            lo = mid;
-        else
-            hi = mid;
+// A warp's walk through tiles of ascending number (weight tiles of a row tile follow one another); all lanes.
+template <int ROWS> struct Walk {
+    const Grouped &g;
+    const int *first;
+    int cols, e;
+    __device__ Walk(const Grouped &G, const int *f, int c) : g(G), first(f), cols(c), e(0) {}
+    __device__ __forceinline__ Tile operator()(int t)
+    {
+        const int m = t / g.ntiles, lane = threadIdx.x & 31;
+        for (;;) { // first[e] <= m < first[e + 1]
+            const unsigned below = __ballot_sync(0xffffffffu, e + 1 + lane <= g.E && first[e + 1 + lane] <= m);
+            e += __popc(below);
+            if (below != 0xffffffffu)
+                break;
+        }
+        e = min(e, g.E - 1);
+        const int2 r = expert_rows(g, e);
+        Tile T;
+        T.e = e;
+        T.row0 = r.x + (m - first[e]) * ROWS;
+        T.rows = min(ROWS, r.y - T.row0);
+        T.col0 = (t % g.ntiles) * cols;
+        return T;
     }
-    const int2 r = expert_rows(g, lo);
-    Tile T;
-    T.e = lo;
-    T.row0 = r.x + (m - first[lo]) * kRows;
-    T.rows = min(kRows, r.y - T.row0);
-    T.col0 = (t % g.ntiles) * cols;
-    return T;
+};
+
+// Rows that the second CTA of a pair has of the tile whose first part is T.
+__device__ __forceinline__ int pair_rows(const Tile &T, const Grouped &g)
+{
+    return T.rows < 128 ? 0 : max(0, min(128, expert_rows(g, T.e).y - T.row0 - 128));
 }
 
 // Prefix sums of the experts' row tiles, first[0..E]; all threads.
-__device__ void row_tiles(const Grouped &g, int *first, int *part)
+template <int ROWS> __device__ void row_tiles(const Grouped &g, int *first, int *part)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (g.E + kThreads - 1) / kThreads;
@@ -162,7 +253,7 @@ __device__ void row_tiles(const Grouped &g, int *first, int *part)
     int sum = 0;
     for (int e = e0; e < e1; ++e) {
         const int2 r = expert_rows(g, e);
-        sum += (r.y - r.x + kRows - 1) / kRows;
+        sum += (r.y - r.x + ROWS - 1) / ROWS;
     }
     int inc = sum;
 #pragma unroll
@@ -179,7 +270,7 @@ __device__ void row_tiles(const Grouped &g, int *first, int *part)
     for (int e = e0; e < e1; ++e) {
         first[e] = at;
         const int2 r = expert_rows(g, e);
-        at += (r.y - r.x + kRows - 1) / kRows;
+        at += (r.y - r.x + ROWS - 1) / ROWS;
     }
     if (tid == kThreads - 1)
         first[g.E] = at; // the last thread's range ends at E
@@ -192,47 +283,128 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, int byt
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// An arrival once all of this thread's copies so far have landed.
-__device__ __forceinline__ void copies_arrive(uint64_t *bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(pipe::smem_u32(bar)) : "memory");
-}
-
 // With the fast exponential and quotient (2 + |g| and 2 units in the last place of a float): far below the
-// rounding of h, and free of branches, so that a thread's 32 columns overlap. (expf and the exact quotient
-// made the epilogue of a 2048-deep q8 tile twice as long as its products.)
+// rounding of h, and free of branches, so that a thread's columns overlap. (expf and the exact quotient made the
+// epilogue of a 2048-deep q8 tile twice as long as its products.)
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-__device__ __forceinline__ uint32_t bf16x2(float a, float b)
+// A warp's part of a stage is there (fenced for the tensor cores).
+template <class S> __device__ __forceinline__ void arrive_full(Bars *bars, int s)
 {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
+    if (S::kPair)
+        arrive_in_first(&bars->full[s]);
+    else
+        pipe::mbar_arrive(&bars->full[s]);
 }
 
-template <bool Q8IN, bool SWIGLU, int NT, int OUT>
-__global__ void __launch_bounds__(kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-                   const __grid_constant__ Grouped g)
+// The scale warps: 32 * ROWS rows, a lane has rows lane + 32 j. The words of four stages (16 bytes of a row) are
+// loaded together, DEPTH such groups ahead of their use. rows_of(T, j) is the row's scale bytes, or NULL where
+// the values are zeros or not used (scale 1, so that zeros stay zeros).
+template <class S, int ROWS, int DEPTH, class RowsOf, class Tiles>
+__device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const Waiter &wait, uint8_t *dst, int tiles,
+                                           int t0, int step, int where, const RowsOf &rows_of, Tiles tile)
 {
-    using S = Shape<Q8IN, NT>;
+    const int lane = threadIdx.x & 31;
+    const int groups = (g.iters + 3) / 4;
+    const bool wide = g.iters % 4 == 0; // rows of scales are 16-byte aligned
+    constexpr uint32_t kOnes = 0x7f7f7f7fu;
+    const uint8_t *row[ROWS];
+    uint4 next[DEPTH][ROWS];
+    int at = t0, group = 0; // the next group to load
+    auto load = [&](uint4(&v)[ROWS]) {
+        if (at >= tiles)
+            return;
+        if (group == 0) {
+            const Tile T = tile(at);
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+                row[j] = rows_of(T, lane + 32 * j);
+        }
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+            v[j] = make_uint4(kOnes, kOnes, kOnes, kOnes);
+            if (row[j]) {
+                const uint32_t *p = reinterpret_cast<const uint32_t *>(row[j]) + 4 * group;
+                if (wide) {
+                    v[j] = __ldg(reinterpret_cast<const uint4 *>(p));
+                } else {
+                    const int left = g.iters - 4 * group;
+                    v[j].x = __ldg(p);
+                    v[j].y = left > 1 ? __ldg(p + 1) : kOnes;
+                    v[j].z = left > 2 ? __ldg(p + 2) : kOnes;
+                    v[j].w = left > 3 ? __ldg(p + 3) : kOnes;
+                }
+            }
+        }
+        if (++group == groups) {
+            group = 0;
+            at += step;
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+        load(next[d]);
+    Ring<S::kStages> ring;
+    for (int t = t0; t < tiles; t += step) {
+        for (int k = 0; k < g.iters; k += 4) {
+            uint4 now[ROWS];
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+                now[j] = next[0][j];
+#pragma unroll
+                for (int d = 1; d < DEPTH; ++d)
+                    next[d - 1][j] = next[d][j];
+            }
+            load(next[DEPTH - 1]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (k + q >= g.iters)
+                    break;
+                if (!ring.free(wait, bars, where))
+                    return;
+                auto word = [&](int j) {
+                    return j >= ROWS ? kOnes : q == 0 ? now[j].x : q == 1 ? now[j].y : q == 2 ? now[j].z : now[j].w;
+                };
+#pragma unroll
+                for (int j = 0; j < ROWS; j += 4)
+                    *reinterpret_cast<uint4 *>(dst + ring.s * S::kScales + 512 * (j / 4) + lane * 16) =
+                        make_uint4(word(j), word(j + 1), word(j + 2), word(j + 3));
+                umma::fence_smem_async();
+                __syncwarp();
+                if (lane == 0)
+                    arrive_full<S>(bars, ring.s);
+                ring.next();
+            }
+        }
+    }
+}
+
+template <bool Q8IN, bool SWIGLU, bool PAIR, int ROWS, int NT, int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xwide,
+                   const __grid_constant__ CUtensorMap wmap, const __grid_constant__ Grouped g)
+{
+    using S = Shape<Q8IN, PAIR, ROWS, NT>;
     constexpr int kCols = SWIGLU ? NT / 2 : NT; // output columns of a tile
-    constexpr int kElem = Q8IN ? 1 : 2;
+    constexpr int kElem = Q8IN ? 1 : 2, kCtas = PAIR ? 2 : 1;
+    constexpr int kBoxRows = SWIGLU ? 64 : 128, kBoxCols = SWIGLU ? 32 : 128; // a box of matrix rows, its columns
+    constexpr int kBoxes = S::kBRows / kBoxRows;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (pipe::smem_u32(raw) & 1023)) & 1023);
     Bars *bars = reinterpret_cast<Bars *>(smem + S::kBarAt);
     int *first = reinterpret_cast<int *>(smem + S::kTableAt);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            pipe::mbar_init(&bars->full[s], 1);
-            pipe::mbar_init(&bars->gathered[s], 32 * kGatherWarps);
-            pipe::mbar_init(&bars->scales[s], 2);
+            // the producer with its bytes; of each CTA, two scale warps and the gather warps
+            pipe::mbar_init(&bars->full[s], 1 + kCtas * ((Q8IN ? 2 : 0) + (g.index ? kGatherWarps : 0)));
             pipe::mbar_init(&bars->empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             pipe::mbar_init(&bars->acc_full[i], 1);
-            pipe::mbar_init(&bars->acc_free[i], 4);
+            pipe::mbar_init(&bars->acc_free[i], 4 * kCtas);
         }
         pipe::mbar_init(&bars->done, 1);
         bars->abort = 0;
@@ -240,217 +412,155 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma::prefetch_map(&xmap);
         tma::prefetch_map(&wmap);
     }
-    if (warp == 1) {
-        umma::tmem_alloc(&bars->tmem, S::kTmemCols);
-        umma::tmem_relinquish();
-    }
+    if (warp == 1)
+        umma::tmem_alloc_group<kCtas>(&bars->tmem, S::kTmemCols);
     umma::fence_before_sync();
-    row_tiles(g, first, bars->part); // ends with the block's barrier
+    row_tiles<kCtas * ROWS>(g, first, bars->part); // ends with the block's barrier
+    if (PAIR)
+        cluster_sync(); // the other CTA's barriers are there
     umma::fence_after_sync();
     const uint32_t tmem = bars->tmem;
-    const int tiles = first[g.E] * g.ntiles;
+    const int tiles = first[g.E] * g.ntiles, t0 = blockIdx.x / kCtas, step = gridDim.x / kCtas;
     const Waiter wait{bars, g.limit_ns};
+    Walk<kCtas * ROWS> walk(g, first, kCols);
+    auto tile = [walk, rank](int t) mutable { // this CTA's rows of a pair's tile (perhaps none)
+        Tile T = walk(t);
+        if (PAIR) {
+            T.row0 += rank * ROWS;
+            T.rows = max(0, min(ROWS, T.rows - rank * ROWS));
+        }
+        return T;
+    };
 
     if (warp == 0) {
-        // ---- producer
-        int it = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-            const Tile T = tile_at(g, first, t, kCols);
-            const int loads = g.index ? 0 : (T.rows + 31) / 32;
-            const uint32_t bytes = (uint32_t)(loads * 32 * kRowBytes + S::kB);
-            const int second = SWIGLU ? g.width + T.col0 : T.col0 + NT / 2;
-            for (int i = 0; i < g.iters; ++i, ++it) {
-                const int s = it % S::kStages, u = it / S::kStages;
-                if (u > 0 && !warp_wait(wait, &bars->empty[s], (u - 1) & 1, 1))
+        // ---- producer. A pair's loads complete on the first CTA's barriers.
+        Ring<S::kStages> ring;
+        for (int t = t0; t < tiles; t += step) {
+            const Tile T = tile(t);
+            const bool one = ROWS == 128 && T.rows > 64; // one box of 128 rows
+            const int loads = g.index ? 0 : one ? 1 : (T.rows + 31) / 32;
+            uint32_t bytes = (uint32_t)(loads * (one ? 128 : 32) * kRowBytes + S::kB);
+            if (PAIR && rank == 0) { // and the second CTA's
+                const int rows = pair_rows(T, g);
+                bytes += (uint32_t)(g.index ? 0 : rows > 64 ? 128 : (rows + 31) / 32 * 32) * kRowBytes + S::kB;
+            }
+            for (int i = 0; i < g.iters; ++i, ring.next()) {
+                const int s = ring.s;
+                if (!ring.free(wait, bars, 1))
                     goto produced;
                 uint8_t *a = smem + s * (S::kA + S::kB), *b = a + S::kA;
                 const int x = i * (kRowBytes / kElem);
-                if (lane == 0)
+                if (lane == 0 && rank == 0)
                     pipe::mbar_arrive_expect_tx(&bars->full[s], bytes);
                 __syncwarp();
-                if (lane < 2)
-                    tma::load_3d(b + lane * (NT / 2) * kRowBytes, &wmap, x, lane ? second : T.col0, T.e,
-                                 &bars->full[s]);
-                if (lane < loads)
-                    tma::load_2d(a + lane * 32 * kRowBytes, &xmap, x, T.row0 + 32 * lane, &bars->full[s]);
-                __syncwarp();
+                const uint32_t full = PAIR ? in_first(&bars->full[s]) : pipe::smem_u32(&bars->full[s]);
+                if (lane < kBoxes)
+                    tma::load_4d<kCtas>(b + lane * kBoxRows * kRowBytes, &wmap, x,
+                                        T.col0 + (rank * kBoxes + lane) * kBoxCols, 0, T.e, full);
+                else if (lane < kBoxes + loads)
+                    tma::load_2d<kCtas>(a + (lane - kBoxes) * 32 * kRowBytes, one ? &xwide : &xmap, x,
+                                        T.row0 + 32 * (lane - kBoxes), full);
             }
         }
     produced:
         __syncwarp();
-        // what was issued has to land before the CTA's shared memory goes
-        for (int j = max(0, it - S::kStages); j < it; ++j)
-            drain(&bars->full[j % S::kStages], (j / S::kStages) & 1);
     } else if (warp == 1) {
-        // ---- MMA
-        if (lane == 0) {
-            int it = 0, i = 0;
-            for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+        // ---- MMA (of a pair, the first CTA's)
+        if (lane == 0 && rank == 0) {
+            Ring<S::kStages> ring;
+            const uint64_t a0 = umma::smem_desc_sw128(smem), b0 = umma::smem_desc_sw128(smem + S::kA);
+            bool ok = true;
+            int i = 0;
+            for (int t = t0; ok && t < tiles; t += step, ++i) {
                 // the accumulator this tile takes: free since the epilogue's read of the last tile's shared
                 // columns (q8, 256 columns), or of all of the tile before that
                 const int free = S::kOverlap ? i - 1 : i - 2;
-                if (free >= 0 && !wait(&bars->acc_free[free & 1], (free >> 1) & 1, 2))
-                    break;
+                ok = free < 0 || wait(&bars->acc_free[free & 1], (free >> 1) & 1, 2);
                 umma::fence_after_sync();
                 const uint32_t d = tmem + (i & 1) * S::kSecond;
-                bool ok = true;
-                for (int k = 0; k < g.iters; ++k, ++it) {
-                    const int s = it % S::kStages, u = it / S::kStages;
-                    if (!wait(&bars->full[s], u & 1, 3) || (Q8IN && !wait(&bars->scales[s], u & 1, 4)) ||
-                        (g.index && !wait(&bars->gathered[s], u & 1, 8))) {
-                        ok = false;
+                for (int k = 0; ok && k < g.iters; ++k, ring.next()) {
+                    const int s = ring.s;
+                    ok = wait(&bars->full[s], ring.phase, 3);
+                    if (!ok)
                         break;
-                    }
-                    if (Q8IN || g.index) // what other threads stored is seen by the tensor cores from here on
-                        umma::fence_smem_async();
                     umma::fence_after_sync();
-                    const uint8_t *a = smem + s * (S::kA + S::kB), *b = a + S::kA;
-                    const uint64_t ad = umma::smem_desc_sw128(a), bd = umma::smem_desc_sw128(b);
+                    const uint64_t ad = a0 + s * ((S::kA + S::kB) >> 4), bd = b0 + s * ((S::kA + S::kB) >> 4);
                     if (Q8IN) {
-                        // two sets of scale columns: the MMAs that read this one are two stages back
-                        if (it >= 2 && !wait(&bars->empty[(it - 2) % S::kStages], ((it - 2) / S::kStages) & 1, 5)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t sa = tmem + S::kScaleCols + 4 * (it & 1);
-                        const uint32_t sb = tmem + S::kScaleCols + 8 + 8 * (it & 1);
-                        const uint8_t *sc = smem + S::kStageAt + s * S::kScales;
-                        umma::copy_scales(sa, sc);
-                        for (int j = 0; j < NT / 128; ++j)
-                            umma::copy_scales(sb + 4 * j, sc + 512 * (j + 1));
+                        // a set of scale columns per stage: what read it last has finished, or the stage would not
+                        // be there
+                        const uint32_t sa = tmem + S::kScaleCols + 4 * s;
+                        const uint32_t sb = tmem + S::kScaleCols + 4 * S::kSets + 4 * S::kAtoms * s;
+                        const uint8_t *sc = smem + S::kScalesAt + s * S::kScales;
+                        umma::copy_scales<kCtas>(sa, sc);
+                        for (int j = 0; j < S::kAtoms; ++j)
+                            umma::copy_scales<kCtas>(sb + 4 * j, sc + 512 * (j + 1));
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            umma::mma_mxf8(d, ad + 2 * j, bd + 2 * j, umma::idesc_mxf8(kRows, NT, j), sa, sb,
-                                           (k | j) != 0);
+                            umma::mma_mxf8<kCtas>(d, ad + 2 * j, bd + 2 * j, umma::idesc_mxf8(kCtas * kLanes, NT, j), sa,
+                                                  sb, (k | j) != 0);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            umma::mma_f16(d, ad + 2 * j, bd + 2 * j, umma::idesc_bf16(kRows, NT), (k | j) != 0);
+                            umma::mma_bf16<kCtas>(d, ad + 2 * j, bd + 2 * j, umma::idesc_bf16(kCtas * kLanes, NT),
+                                                  (k | j) != 0);
                     }
-                    umma::commit(&bars->empty[s]);
+                    umma::commit_group<kCtas>(&bars->empty[s]);
                 }
-                if (!ok)
-                    break;
-                umma::commit(&bars->acc_full[i & 1]);
+                if (ok)
+                    umma::commit_group<kCtas>(&bars->acc_full[i & 1]);
             }
-            umma::commit(&bars->done);
+            umma::commit_local<kCtas>(&bars->done);
             drain(&bars->done, 0);
         }
         __syncwarp();
-    } else if (warp < 4) {
-        // ---- scale bytes: warp 2 the input rows', warp 3 the matrix rows'. A lane has rows lane + 32 j; a
-        // group of four stages' words (16 bytes per row) is loaded while the group before is handed over.
-        if (Q8IN) {
-            constexpr int kMost = NT / 32;
-            const bool mine = warp == 2; // input rows
-            const int have = mine ? 4 : kMost;
-            const int64_t words = g.K / 128;
-            const int groups = (g.iters + 3) / 4;
-            const bool wide = g.iters % 4 == 0; // rows of scales are 16-byte aligned
-            const uint8_t *row[kMost < 4 ? 4 : kMost];
-            uint4 next[kMost < 4 ? 4 : kMost];
-            const uint32_t kOnes = 0x7f7f7f7fu;
-
-            auto rows_of = [&](int t) {
-                const Tile T = tile_at(g, first, t, kCols);
-#pragma unroll
-                for (int j = 0; j < (kMost < 4 ? 4 : kMost); ++j) {
-                    if (j >= have)
-                        break;
-                    const int r = lane + 32 * j;
-                    row[j] = nullptr;
-                    if (mine) {
-                        if (r < T.rows) {
-                            const int i = g.index ? __ldg(g.index + T.row0 + r) : T.row0 + r;
-                            if ((uint32_t)i < (uint32_t)g.n)
-                                row[j] = g.xs + (int64_t)i * words * 4;
-                        }
-                    } else {
-                        const int c = r < NT / 2 ? T.col0 + r
-                                                 : (SWIGLU ? g.width + T.col0 : T.col0 + NT / 2) + r - NT / 2;
-                        if (c < g.N)
-                            row[j] = g.ws + ((int64_t)T.e * g.N + c) * words * 4;
-                    }
-                }
-            };
-            auto load = [&](int group) {
-#pragma unroll
-                for (int j = 0; j < (kMost < 4 ? 4 : kMost); ++j) {
-                    if (j >= have)
-                        break;
-                    uint4 v = make_uint4(kOnes, kOnes, kOnes, kOnes);
-                    if (row[j]) {
-                        const uint32_t *p = reinterpret_cast<const uint32_t *>(row[j]) + 4 * group;
-                        if (wide) {
-                            v = __ldg(reinterpret_cast<const uint4 *>(p));
-                        } else {
-                            const int left = g.iters - 4 * group;
-                            v.x = __ldg(p);
-                            v.y = left > 1 ? __ldg(p + 1) : kOnes;
-                            v.z = left > 2 ? __ldg(p + 2) : kOnes;
-                            v.w = left > 3 ? __ldg(p + 3) : kOnes;
-                        }
-                    }
-                    next[j] = v;
-                }
-            };
-
-            int it = 0, t = blockIdx.x, group = 0;
-            if (t < tiles) {
-                rows_of(t);
-                load(0);
-            }
-            while (t < tiles) {
-                uint4 now[kMost < 4 ? 4 : kMost];
-#pragma unroll
-                for (int j = 0; j < (kMost < 4 ? 4 : kMost); ++j)
-                    now[j] = next[j];
-                const int count = min(4, g.iters - 4 * group);
-                if (++group == groups) {
-                    group = 0;
-                    t += gridDim.x;
-                    if (t < tiles)
-                        rows_of(t);
-                }
-                if (t < tiles)
-                    load(group);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q >= count)
-                        break;
-                    const int s = it % S::kStages, u = it / S::kStages;
-                    if (u > 0 && !warp_wait(wait, &bars->empty[s], (u - 1) & 1, 6))
-                        goto scaled;
-                    uint8_t *sc = smem + S::kStageAt + s * S::kScales + (mine ? 0 : 512) + lane * 16;
-#pragma unroll
-                    for (int j = 0; j < (kMost < 4 ? 4 : kMost); j += 4) {
-                        if (j >= have)
-                            break;
-                        auto word = [&](const uint4 &v) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; };
-                        *reinterpret_cast<uint4 *>(sc + 512 * (j / 4)) =
-                            make_uint4(word(now[j]), word(now[j + 1]), word(now[j + 2]), word(now[j + 3]));
-                    }
-                    __syncwarp();
-                    if (lane == 0)
-                        pipe::mbar_arrive(&bars->scales[s]);
-                    ++it;
-                }
-            }
-        scaled:
-            __syncwarp();
-        }
+    } else if (warp == 2) {
+        // ---- scale bytes of the rows of x
+        if (Q8IN)
+            scale_warp<S, ROWS / 32, 3>(
+                g, bars, wait, smem + S::kScalesAt, tiles, t0, step, 6,
+                [&](const Tile &T, int r) -> const uint8_t * {
+                    if (r >= T.rows)
+                        return nullptr;
+                    const int i = g.index ? __ldg(g.index + T.row0 + r) : T.row0 + r;
+                    return (uint32_t)i < (uint32_t)g.n ? g.xs + (int64_t)i * (g.K / 32) : nullptr;
+                },
+                tile);
+        __syncwarp();
+    } else if (warp == 3) {
+        // ---- scale bytes of the matrix rows
+        if (Q8IN)
+            scale_warp<S, NT / 32, NT == 256 ? 2 : 3>(
+                g, bars, wait, smem + S::kScalesAt + 512, tiles, t0, step, 7,
+                [&](const Tile &T, int r) -> const uint8_t * {
+                    const bool up = SWIGLU && (r & 32);
+                    const int c = T.col0 + (SWIGLU ? (r / 64) * 32 + (r & 31) : r);
+                    return c < g.width ? g.ws + ((int64_t)T.e * g.N + c + (up ? g.width : 0)) * (g.K / 32) : nullptr;
+                },
+                tile);
+        __syncwarp();
     } else if (warp >= 8) {
-        // ---- gathered input rows: a thread has one 16-byte chunk of rows r0, r0 + 16, ...
+        // ---- gathered rows of x: a thread has one 16-byte chunk of rows r0, r0 + 16, ... A stage is handed over
+        // once the copies of two more have been issued.
         if (g.index) {
+            constexpr int kLag = 2;
             const int r0 = (warp - 8) * 4 + lane / 8, chunk = lane & 7;
             const int64_t pitch = (int64_t)g.K * kElem;
             const uint32_t at = (uint32_t)(r0 * kRowBytes + ((chunk ^ (r0 & 7)) << 4)); // 16 more rows: 2 KB more
-            int it = 0;
-            for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-                const Tile T = tile_at(g, first, t, kCols);
-                const uint8_t *src[kRows / 16];
+            Ring<S::kStages> ring, behind;
+            int ahead = 0; // stages issued and not handed over
+            auto hand_over = [&] {
+                umma::fence_smem_async();
+                __syncwarp();
+                if (lane == 0)
+                    arrive_full<S>(bars, behind.s);
+                behind.next();
+                --ahead;
+            };
+            for (int t = t0; t < tiles; t += step) {
+                const Tile T = tile(t);
+                const uint8_t *src[ROWS / 16];
 #pragma unroll
-                for (int j = 0; j < kRows / 16; ++j) {
+                for (int j = 0; j < ROWS / 16; ++j) {
                     const int r = r0 + 16 * j;
                     src[j] = nullptr;
                     if (r < T.rows) {
@@ -459,38 +569,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                             src[j] = g.x + i * pitch + 16 * chunk;
                     }
                 }
-                for (int i = 0; i < g.iters; ++i, ++it) {
-                    const int s = it % S::kStages, u = it / S::kStages;
-                    if (u > 0 && !warp_wait(wait, &bars->empty[s], (u - 1) & 1, 9))
+                for (int i = 0; i < g.iters; ++i, ring.next()) {
+                    if (!ring.free(wait, bars, 9))
                         goto gathered;
-                    const uint32_t dst = pipe::smem_u32(smem + s * (S::kA + S::kB)) + at;
+                    const uint32_t dst = pipe::smem_u32(smem + ring.s * (S::kA + S::kB)) + at;
                     const bool in = i * kRowBytes + 16 * chunk < pitch;
 #pragma unroll
-                    for (int j = 0; j < kRows / 16; ++j)
+                    for (int j = 0; j < ROWS / 16; ++j)
                         if (r0 + 16 * j < T.rows) // rows outside x, and k behind K, are filled with zeros
                             copy16(dst + j * 16 * kRowBytes, src[j] && in ? src[j] + i * kRowBytes : g.x,
                                    src[j] && in ? 16 : 0);
-                    copies_arrive(&bars->gathered[s]);
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (++ahead > kLag) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+                        hand_over();
+                    }
                 }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            while (ahead > 0)
+                hand_over();
         gathered:
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
         }
     } else {
-        // ---- epilogue
-        constexpr int kChunks = kCols / 32;
-        constexpr int kUnits = OUT == PMOE_TYPE_F32 ? 8 : OUT == PMOE_TYPE_BF16 ? 4 : 2; // 16-byte units of a chunk
-        constexpr int kPer = kChunks < 8 / kUnits ? kChunks : 8 / kUnits;                // chunks stored together
-        constexpr int kPitch = kPer * kUnits;                                            // units of a staged row
+        // ---- epilogue, 64 accumulator columns at a time: 64 output columns, or 32 of a SwiGLU
+        constexpr int kChunks = NT / 64, kHalves = SWIGLU ? 1 : 2; // halves: 32 output columns
+        constexpr int kUnits = OUT == PMOE_TYPE_F32 ? 8 : OUT == PMOE_TYPE_BF16 ? 4 : 2; // 16-byte units of a half
+        constexpr int kAll = kChunks * kHalves;
+        constexpr int kPer = kAll < 8 / kUnits ? kAll : 8 / kUnits; // halves stored together
+        constexpr int kPitch = kPer * kUnits;                       // units of a staged row
         constexpr int kUnitCols = 32 / kUnits;
         const int q = warp & 3;
         uint8_t *stage = smem + S::kStagingAt + q * 32 * kStageRowBytes;
         auto place = [&](int r, int unit) { return stage + (r * kPitch + (unit ^ (r & (kPitch - 1)))) * 16; };
         int i = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
-            const Tile T = tile_at(g, first, t, kCols);
-            if (!warp_wait(wait, &bars->acc_full[i & 1], (i >> 1) & 1, 7))
+        for (int t = t0; t < tiles; t += step, ++i) {
+            const Tile T = tile(t);
+            if (!warp_wait(wait, &bars->acc_full[i & 1], (i >> 1) & 1, 10))
                 break;
             umma::fence_after_sync();
             const uint32_t acc = tmem + (i & 1) * S::kSecond + ((uint32_t)(32 * q) << 16);
@@ -499,90 +616,111 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < kChunks; ++j) {
                 const int c = backwards ? kChunks - 1 - j : j;
-                float v[32], w[32];
-                if (any) {
-                    umma::ld32(acc + 32 * c, v);
-                    if (SWIGLU)
-                        umma::ld32(acc + NT / 2 + 32 * c, w);
-                }
+                float v[64];
+                if (any)
+                    umma::ld64(acc + 64 * c, v);
                 if (j == (S::kOverlap ? 0 : kChunks - 1)) {
                     umma::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0)
-                        pipe::mbar_arrive(&bars->acc_free[i & 1]);
-                }
-                if (!any || T.col0 + 32 * c >= g.width)
-                    continue;
-                if (SWIGLU) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        v[x] = silu(v[x]) * w[x];
-                }
-                const int base = (c % kPer) * kUnits;
-                if (OUT == PMOE_TYPE_F32) {
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        *reinterpret_cast<float4 *>(place(lane, base + x)) =
-                            make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                } else if (OUT == PMOE_TYPE_BF16) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        *reinterpret_cast<uint4 *>(place(lane, base + x)) =
-                            make_uint4(bf16x2(v[8 * x], v[8 * x + 1]), bf16x2(v[8 * x + 2], v[8 * x + 3]),
-                                       bf16x2(v[8 * x + 4], v[8 * x + 5]), bf16x2(v[8 * x + 6], v[8 * x + 7]));
-                } else {
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        top = max(top, q8::magnitude(v[x]));
-                    const uint32_t byte = q8::scale_byte(top);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            o[y] = q8::codes4(v[16 * x + 4 * y], v[16 * x + 4 * y + 1], v[16 * x + 4 * y + 2],
-                                              v[16 * x + 4 * y + 3], byte);
-                        *reinterpret_cast<uint4 *>(place(lane, base + x)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (lane == 0) {
+                        if (PAIR)
+                            arrive_in_first(&bars->acc_free[i & 1]);
+                        else
+                            pipe::mbar_arrive(&bars->acc_free[i & 1]);
                     }
-                    if (32 * q + lane < T.rows)
-                        g.out_scales[(int64_t)(T.row0 + 32 * q + lane) * (g.width / 32) + T.col0 / 32 + c] =
-                            (uint8_t)byte;
                 }
-                // the group's last chunk in this order, or the last one inside the matrix
-                const bool last = backwards ? c % kPer == 0
-                                            : c % kPer == kPer - 1 || T.col0 + 32 * (c + 1) >= g.width;
-                if (!last)
+                if (!any)
                     continue;
-                __syncwarp();
-                const int unit = lane % kPitch;
-                const int col = T.col0 + 32 * (c - c % kPer) + unit * kUnitCols;
 #pragma unroll
-                for (int x = 0; x < kPitch; ++x) {
-                    const int r = lane / kPitch + x * (32 / kPitch);
-                    if (32 * q + r < T.rows && col < g.width)
-                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(g.out) +
-                                                   ((int64_t)(T.row0 + 32 * q + r) * g.width + col) *
-                                                       (16 / kUnitCols)) =
-                            *reinterpret_cast<const uint4 *>(place(r, unit));
+                for (int half = 0; half < kHalves; ++half) {
+                    const int h = kHalves * c + half; // 32 output columns
+                    if (T.col0 + 32 * h >= g.width)
+                        continue;
+                    float *o = v + 32 * half;
+                    if (SWIGLU) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            o[x] = silu(o[x]) * v[32 + x];
+                    }
+                    const int base = (h % kPer) * kUnits;
+                    if (OUT == PMOE_TYPE_F32) {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            *reinterpret_cast<float4 *>(place(lane, base + x)) =
+                                make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    } else if (OUT == PMOE_TYPE_BF16) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            *reinterpret_cast<uint4 *>(place(lane, base + x)) =
+                                make_uint4(bf16x2(o[8 * x], o[8 * x + 1]), bf16x2(o[8 * x + 2], o[8 * x + 3]),
+                                           bf16x2(o[8 * x + 4], o[8 * x + 5]), bf16x2(o[8 * x + 6], o[8 * x + 7]));
+                    } else {
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            top = max(top, q8::magnitude(o[x]));
+                        const uint32_t byte = q8::scale_byte(top);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                w[y] = q8::codes4(o[16 * x + 4 * y], o[16 * x + 4 * y + 1], o[16 * x + 4 * y + 2],
+                                                  o[16 * x + 4 * y + 3], byte);
+                            *reinterpret_cast<uint4 *>(place(lane, base + x)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        if (32 * q + lane < T.rows)
+                            g.out_scales[(int64_t)(T.row0 + 32 * q + lane) * (g.width / 32) + T.col0 / 32 + h] =
+                                (uint8_t)byte;
+                    }
+                    // stored together with the last half of the group in this order (or of the matrix)
+                    const bool last = backwards && kHalves == 1
+                                          ? h % kPer == 0
+                                          : h % kPer == kPer - 1 || T.col0 + 32 * (h + 1) >= g.width;
+                    if (!last)
+                        continue;
+                    __syncwarp();
+                    const int unit = lane % kPitch;
+                    const int col = T.col0 + 32 * (h - h % kPer) + unit * kUnitCols;
+#pragma unroll
+                    for (int x = 0; x < kPitch; ++x) {
+                        const int r = lane / kPitch + x * (32 / kPitch);
+                        if (32 * q + r < T.rows && col < g.width)
+                            *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(g.out) +
+                                                       ((int64_t)(T.row0 + 32 * q + r) * g.width + col) *
+                                                           (16 / kUnitCols)) =
+                                *reinterpret_cast<const uint4 *>(place(r, unit));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
     }
+    __syncwarp();
+    if (*reinterpret_cast<volatile int *>(&bars->abort)) // loads that nobody waited for land meanwhile
+        for (const uint64_t until = pipe::globaltimer() + kSettleNs; pipe::globaltimer() < until;) {
+        }
+    __syncwarp();
     umma::fence_before_sync();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync(); // neither CTA's shared or tensor memory goes while the other uses it
+    else
+        __syncthreads();
     if (warp == 1) {
         umma::fence_after_sync();
-        umma::tmem_dealloc(tmem, S::kTmemCols);
+        umma::tmem_dealloc_group<kCtas>(tmem, S::kTmemCols);
     }
 }
 
-template <bool Q8IN, bool SWIGLU, int NT, int OUT>
-pmoe_status launch(const CUtensorMap &xmap, const CUtensorMap &wmap, const Grouped &g, int64_t tiles, cudaStream_t st)
+struct Maps {
+    CUtensorMap x, xwide, w;
+};
+
+template <bool Q8IN, bool SWIGLU, bool PAIR, int ROWS, int NT, int OUT>
+pmoe_status launch(const Maps &m, const Grouped &g, int64_t tiles, cudaStream_t st)
 {
-    using S = Shape<Q8IN, NT>;
-    auto *kernel = grouped_kernel<Q8IN, SWIGLU, NT, OUT>;
+    using S = Shape<Q8IN, PAIR, ROWS, NT>;
+    auto *kernel = grouped_kernel<Q8IN, SWIGLU, PAIR, ROWS, NT, OUT>;
     static std::atomic<uint64_t> ready{0}; // devices whose shared-memory limit of this kernel is set
     int dev = 0;
     PMOE_CUDA(cudaGetDevice(&dev));
@@ -592,20 +730,48 @@ pmoe_status launch(const CUtensorMap &xmap, const CUtensorMap &wmap, const Group
         if (dev < 64)
             ready.fetch_or(1ull << dev);
     }
-    kernel<<<(unsigned)(tiles < kNumSMs ? tiles : kNumSMs), kThreads, S::smem(g.E), st>>>(xmap, wmap, g);
-    return launch_status();
+    constexpr int kCtas = PAIR ? 2 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles < kNumSMs / kCtas ? tiles * kCtas : kNumSMs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::smem(g.E);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, m.x, m.xwide, m.w, g));
 }
 
-template <bool Q8IN, int NT>
-pmoe_status launch_out(bool swiglu, int out_type, const CUtensorMap &xmap, const CUtensorMap &wmap, const Grouped &g,
-                       int64_t tiles, cudaStream_t st)
+template <bool Q8IN, bool PAIR, int ROWS, int NT>
+pmoe_status launch_out(bool swiglu, int out_type, const Maps &m, const Grouped &g, int64_t tiles, cudaStream_t st)
 {
     if (swiglu)
-        return out_type == PMOE_TYPE_Q8 ? launch<Q8IN, true, NT, PMOE_TYPE_Q8>(xmap, wmap, g, tiles, st)
-                                        : launch<Q8IN, true, NT, PMOE_TYPE_BF16>(xmap, wmap, g, tiles, st);
-    return out_type == PMOE_TYPE_F32 ? launch<Q8IN, false, NT, PMOE_TYPE_F32>(xmap, wmap, g, tiles, st)
-                                     : launch<Q8IN, false, NT, PMOE_TYPE_BF16>(xmap, wmap, g, tiles, st);
+        return out_type == PMOE_TYPE_Q8 ? launch<Q8IN, true, PAIR, ROWS, NT, PMOE_TYPE_Q8>(m, g, tiles, st)
+                                        : launch<Q8IN, true, PAIR, ROWS, NT, PMOE_TYPE_BF16>(m, g, tiles, st);
+    return out_type == PMOE_TYPE_F32 ? launch<Q8IN, false, PAIR, ROWS, NT, PMOE_TYPE_F32>(m, g, tiles, st)
+                                     : launch<Q8IN, false, PAIR, ROWS, NT, PMOE_TYPE_BF16>(m, g, tiles, st);
 }
+
+template <bool Q8IN>
+pmoe_status launch_shape(int tile_rows, int nt, bool swiglu, int out_type, const Maps &m, const Grouped &g,
+                         int64_t tiles, cudaStream_t st)
+{
+    if (tile_rows == 256)
+        return launch_out<Q8IN, true, 128, 256>(swiglu, out_type, m, g, tiles, st);
+    if (tile_rows == 32)
+        return nt == 128 ? launch_out<Q8IN, false, 32, 128>(swiglu, out_type, m, g, tiles, st)
+                         : launch_out<Q8IN, false, 32, 256>(swiglu, out_type, m, g, tiles, st);
+    return nt == 128 ? launch_out<Q8IN, false, 128, 128>(swiglu, out_type, m, g, tiles, st)
+                     : launch_out<Q8IN, false, 128, 256>(swiglu, out_type, m, g, tiles, st);
+}
+
+// Rows per expert from which a pair's tiles of 256 rows are faster than single tiles of 128: a stage of the pair
+// takes 0.92 of a single one's time (bf16 1391 against 1292 TFLOP/s, q8 2236 against 2162, at 1024 rows an
+// expert), but an expert's last tile wastes 128 rows on average instead of 64.
+constexpr int kPairRows = 700;
 
 pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offsets, int rows, int out_type, void *out,
                     uint8_t *out_scales, bool swiglu, pmoe_stream stream)
@@ -633,36 +799,40 @@ pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offs
         return PMOE_OK;
     PMOE_TRY(on_current_device({W->w, W->scales, X->x, X->scales, X->index, offsets, out, out_scales}));
 
-    // Row tiles: at most one ragged one per expert. Narrow weight tiles where wide ones leave SMs idle.
-    const int64_t most = (int64_t)rows / kRows + (W->E < rows ? W->E : rows);
+    // Rows of x per tile by the rows an expert has on average; matrix rows per tile by whether 256 give half of
+    // the SMs a tile.
+    const int hit = W->E < rows ? W->E : rows;
+    const int tile_rows = rows <= 16 * (int64_t)hit ? 32 : rows < kPairRows * (int64_t)hit ? 128 : 256;
+    const int64_t most = (int64_t)rows / tile_rows + hit; // at most one ragged row tile per expert
     const int wide = swiglu ? 128 : 256;
-    const bool narrow = most * ((width + wide - 1) / wide) < 2 * kNumSMs;
-    const int cols = narrow ? wide / 2 : wide;
+    const int nt = tile_rows < 256 && most * ((width + wide - 1) / wide) < kNumSMs / 2 ? 128 : 256;
+    const int cols = swiglu ? nt / 2 : nt;
     const int ntiles = (width + cols - 1) / cols;
     // offsets that overlap could name every row for every expert: even those tiles are counted in an int
-    if (((int64_t)rows + kRows - 1) / kRows * W->E * ntiles > INT32_MAX)
+    if (((int64_t)rows + tile_rows - 1) / tile_rows * W->E * ntiles > INT32_MAX)
         return PMOE_ERR_UNSUPPORTED;
     const int elem = is_q8 ? 1 : 2;
     const uint64_t K = (uint64_t)W->K;
-    CUtensorMap xmap, wmap;
+    Maps m;
     // no input rows at all: every index is outside, the map's one row is never read
     const void *x = X->n ? X->x : W->w;
     const uint64_t xd[2] = {K, (uint64_t)(X->n ? X->n : 1)}, xstride[1] = {K * elem};
-    const uint32_t xbox[2] = {(uint32_t)(kRowBytes / elem), 32u};
-    PMOE_TRY(tma::make_map(&xmap, elem, 2, x, xd, xstride, xbox));
-    const uint64_t wd[3] = {K, (uint64_t)W->N, (uint64_t)W->E}, wstride[2] = {K * elem, K * elem * W->N};
-    const uint32_t wbox[3] = {(uint32_t)(kRowBytes / elem), narrow ? 64u : 128u, 1u};
-    PMOE_TRY(tma::make_map(&wmap, elem, 3, W->w, wd, wstride, wbox));
+    const uint32_t xbox[2] = {(uint32_t)(kRowBytes / elem), 32}, xwbox[2] = {(uint32_t)(kRowBytes / elem), 128};
+    PMOE_TRY(tma::make_map(&m.x, elem, 2, x, xd, xstride, xbox));
+    PMOE_TRY(tma::make_map(&m.xwide, elem, 2, x, xd, xstride, xwbox));
+    // [E][gate, up][I][K] in boxes of 32 gate rows and the up rows of the same columns, or [E][1][N][K]
+    const uint64_t halves = swiglu ? 2 : 1;
+    const uint64_t wd[4] = {K, (uint64_t)width, halves, (uint64_t)W->E};
+    const uint64_t wstride[3] = {K * elem, K * elem * width, K * elem * W->N};
+    const uint32_t wbox[4] = {(uint32_t)(kRowBytes / elem), swiglu ? 32u : 128u, (uint32_t)halves, 1};
+    PMOE_TRY(tma::make_map(&m.w, elem, 4, W->w, wd, wstride, wbox));
     const Grouped g{W->E,      W->N,     W->K,      X->n,    rows, width,      (int)((K * elem + kRowBytes - 1) / kRowBytes),
                     ntiles, static_cast<const uint8_t *>(x), W->scales, X->scales, X->index, offsets, out, out_scales,
                     wait_limit_ns()};
     const int64_t tiles = most * ntiles;
     const cudaStream_t st = (cudaStream_t)stream;
-    if (is_q8)
-        return narrow ? launch_out<true, 128>(swiglu, out_type, xmap, wmap, g, tiles, st)
-                      : launch_out<true, 256>(swiglu, out_type, xmap, wmap, g, tiles, st);
-    return narrow ? launch_out<false, 128>(swiglu, out_type, xmap, wmap, g, tiles, st)
-                  : launch_out<false, 256>(swiglu, out_type, xmap, wmap, g, tiles, st);
+    return is_q8 ? launch_shape<true>(tile_rows, nt, swiglu, out_type, m, g, tiles, st)
+                 : launch_shape<false>(tile_rows, nt, swiglu, out_type, m, g, tiles, st);
 }
 
 } // namespace

@@ -40,20 +40,36 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
+// Loads into this CTA's shared memory, completed in bytes on the barrier at address bar: this CTA's, or with
+// CTAS = 2 (a pair of neighbouring CTAs) one of the pair's first CTA.
+template <int CTAS>
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-                 "[%4];" ::"r"(pipe::smem_u32(dst)),
-                 "l"(map), "r"(x), "r"(y), "r"(pipe::smem_u32(bar))
-                 : "memory");
+    if (CTAS == 2)
+        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3}], [%4];" ::"r"(pipe::smem_u32(dst)),
+                     "l"(map), "r"(x), "r"(y), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+                     "%3}], [%4];" ::"r"(pipe::smem_u32(dst)),
+                     "l"(map), "r"(x), "r"(y), "r"(bar)
+                     : "memory");
 }
 
-__device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
+template <int CTAS>
+__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-                 "%4}], [%5];" ::"r"(pipe::smem_u32(dst)),
-                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(pipe::smem_u32(bar))
-                 : "memory");
+    if (CTAS == 2)
+        asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(pipe::smem_u32(dst)),
+                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+                     "%3, %4, %5}], [%6];" ::"r"(pipe::smem_u32(dst)),
+                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+                     : "memory");
 }
 
 } // namespace tma
