@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 
 #include "common.h"
+#include "pipe.cuh"
 
 namespace pmoe {
 
@@ -26,6 +27,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_histogram_kernel(const in
     extern __shared__ int32_t h[];
     for (int e = threadIdx.x; e < E; e += kGroupThreads)
         h[e] = 0;
+    pipe::launch_dependents();
+    pipe::wait_prerequisites();
     __syncthreads();
     const int p0 = blockIdx.x * chunk, p1 = min(P - p0, chunk) + p0;
     for (int p = p0 + threadIdx.x; p < p1; p += kGroupThreads) {
@@ -55,6 +58,8 @@ __global__ void __launch_bounds__(kGroupThreads)
     const int w0 = min(p0 + warp * per, p1), w1 = min(w0 + per, p1);
     for (int i = tid; i < kGroupWarps * E; i += kGroupThreads)
         cnt[i] = 0;
+    pipe::launch_dependents();
+    pipe::wait_prerequisites();
     __syncthreads();
     int32_t *mine = cnt + warp * E;
     for (int p = w0; p < w1; p += 32) {
@@ -162,6 +167,8 @@ __global__ void __launch_bounds__(128)
     if (c >= H)
         return;
     float s[8] = {};
+    pipe::launch_dependents();
+    pipe::wait_prerequisites();
 #pragma unroll 4
     for (int i = 0; i < k; ++i) {
         const int row = __ldg(row_of + (int64_t)t * k + i);
@@ -216,10 +223,10 @@ pmoe_status pmoe_group_pairs(const int32_t *ids, int T, int k, int E, int32_t *o
                                        kGroupWarps * kMaxGroupExperts * (int)sizeof(int32_t)));
     int32_t *hist = blocks > 1 ? static_cast<int32_t *>(ws) : nullptr;
     if (hist)
-        group_histogram_kernel<<<blocks, kGroupThreads, E * sizeof(int32_t), st>>>(ids, (int)P, E, chunk, hist);
-    group_scatter_kernel<<<blocks, kGroupThreads, smem, st>>>(ids, (int)P, k, E, chunk, hist, offsets, row_of,
-                                                              token_of);
-    return launch_status();
+        PMOE_TRY(launch_early(group_histogram_kernel, dim3(blocks), kGroupThreads, E * sizeof(int32_t), st, 1, ids, (int)P,
+                              E, chunk, hist));
+    return launch_early(group_scatter_kernel, dim3(blocks), kGroupThreads, smem, st, 1, ids, (int)P, k, E, chunk, hist,
+                        offsets, row_of, token_of);
 }
 
 pmoe_status pmoe_combine_rows(const void *rows, int rows_are_bf16, const int32_t *row_of, const float *w, int T, int k,
@@ -235,12 +242,8 @@ pmoe_status pmoe_combine_rows(const void *rows, int rows_are_bf16, const int32_t
     if (T == 0)
         return PMOE_OK;
     PMOE_TRY(on_current_device({rows, row_of, w, y}));
-    const int grid = T * chunks;
-    if (rows_are_bf16)
-        combine_rows_kernel<true><<<grid, 128, 0, (cudaStream_t)stream>>>(rows, row_of, w, (int)P, k, H, chunks, y);
-    else
-        combine_rows_kernel<false><<<grid, 128, 0, (cudaStream_t)stream>>>(rows, row_of, w, (int)P, k, H, chunks, y);
-    return launch_status();
+    return launch_early(rows_are_bf16 ? combine_rows_kernel<true> : combine_rows_kernel<false>, dim3(T * chunks), 128, 0,
+                        (cudaStream_t)stream, 1, rows, row_of, w, (int)P, k, H, chunks, y);
 }
 
 } // extern "C"

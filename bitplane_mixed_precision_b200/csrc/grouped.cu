@@ -66,6 +66,7 @@ struct Grouped {
 };
 
 constexpr int kMostStages = 12;
+
 template <bool Q8IN, bool PAIR, int ROWS, int NT> struct Shape {
     static_assert(!PAIR || (ROWS == 128 && NT == 256), "shapes");
     static constexpr bool kPair = PAIR;
@@ -73,7 +74,8 @@ template <bool Q8IN, bool PAIR, int ROWS, int NT> struct Shape {
     static constexpr int kA = ROWS * kRowBytes, kB = kBRows * kRowBytes;
     static constexpr int kAtoms = NT / 128; // scale blocks of 128 matrix rows (a pair's CTAs have all of them)
     static constexpr int kScales = Q8IN ? 512 * (1 + kAtoms) : 0;
-    static constexpr int kStaging = 4 * 32 * kStageRowBytes;
+    static constexpr int kStaging = ROWS == 32 ? 32 * 132 * 4 : 4 * 32 * kStageRowBytes;
+    static constexpr int kStagingPitch = 132; // ROWS = 32: floats of a staged row of 128 columns
     // the MMA reads 128 rows from a stage's rows of x even when it has 32 (the lanes of the others are not used):
     // what follows has to be there
     static constexpr int kPad = (kLanes - ROWS) * kRowBytes > kB ? (kLanes - ROWS) * kRowBytes - kB : 0;
@@ -221,13 +223,13 @@ template <int ROWS> struct Walk {
     __device__ __forceinline__ Tile operator()(int t)
     {
         const int m = t / g.ntiles, lane = threadIdx.x & 31;
-        for (;;) { // first[e] <= m < first[e + 1]
-            const unsigned below = __ballot_sync(0xffffffffu, e + 1 + lane <= g.E && first[e + 1 + lane] <= m);
-            e += __popc(below);
-            if (below != 0xffffffffu)
-                break;
+        int end = g.E; // first[e] <= m < first[end]: 32 places of the range at a time
+        while (end - e > 1) {
+            const int span = (end - e + 31) / 32, at = min(e + (lane + 1) * span, end);
+            const int below = __popc(__ballot_sync(0xffffffffu, first[at] <= m));
+            e += below * span;
+            end = min(e + span, end);
         }
-        e = min(e, g.E - 1);
         const int2 r = expert_rows(g, e);
         Tile T;
         T.e = e;
@@ -287,6 +289,23 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, int byt
 // rounding of h, and free of branches, so that a thread's columns overlap. (expf and the exact quotient made the
 // epilogue of a 2048-deep q8 tile twice as long as its products.)
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// Barrier of the four epilogue warps; between two of them none waits for anything that has a limit.
+__device__ __forceinline__ void epilogue_sync() { pipe::named_bar(1, 128); }
+
+// The same, with one answer for all: whether all are to go on.
+__device__ __forceinline__ bool epilogue_all(bool ok)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)ok)
+                 : "memory");
+    return r != 0;
+}
 
 // A warp's part of a stage is there (fenced for the tensor cores).
 template <class S> __device__ __forceinline__ void arrive_full(Bars *bars, int s)
@@ -414,6 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1)
         umma::tmem_alloc_group<kCtas>(&bars->tmem, S::kTmemCols);
+    pipe::launch_dependents();
+    pipe::wait_prerequisites(); // nothing of another launch is read or written before this
     umma::fence_before_sync();
     row_tiles<kCtas * ROWS>(g, first, bars->part); // ends with the block's barrier
     if (PAIR)
@@ -593,6 +614,78 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
         }
+    } else if (ROWS == 32) {
+        // ---- epilogue of few rows: one warp has them all in its lanes, so it only brings the accumulators to
+        // shared memory, 128 columns at a time, and all four warps go on from there (one warp alone took 3.8 us
+        // for a row of 256 columns with SwiGLU and q8)
+        constexpr int kParts = NT / 128, kGroups = SWIGLU ? 16 : 32; // four output columns each
+        const int q = warp & 3;
+        float *stage = reinterpret_cast<float *>(smem + S::kStagingAt);
+        int i = 0;
+        for (int t = t0; t < tiles; t += step, ++i) {
+            const Tile T = tile(t);
+            if (!epilogue_all(warp_wait(wait, &bars->acc_full[i & 1], (i >> 1) & 1, 10)))
+                break;
+            umma::fence_after_sync();
+            const bool backwards = S::kOverlap && (i & 1) == 0; // the shared columns first
+#pragma unroll 1
+            for (int j = 0; j < kParts; ++j) {
+                const int part = backwards ? kParts - 1 - j : j;
+                if (q == 0) {
+                    const uint32_t acc = tmem + (i & 1) * S::kSecond + 128 * part;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float v[64];
+                        umma::ld64(acc + 64 * half, v);
+                        if (lane < T.rows)
+#pragma unroll
+                            for (int x = 0; x < 16; ++x)
+                                *reinterpret_cast<float4 *>(stage + lane * S::kStagingPitch + 64 * half + 4 * x) =
+                                    make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                    }
+                }
+                if (j == (S::kOverlap ? 0 : kParts - 1)) { // kOverlap: the shared 64 columns are in the first part
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        pipe::mbar_arrive(&bars->acc_free[i & 1]);
+                }
+                epilogue_sync();
+                for (int at0 = 32 * q; at0 < T.rows * kGroups; at0 += 128) {
+                    const int at = at0 + lane, r = at / kGroups, group = at % kGroups;
+                    const int staged = SWIGLU ? group / 8 * 64 + group % 8 * 4 : 4 * group;
+                    const int col = T.col0 + 4 * (part * kGroups + group);
+                    const bool in = r < T.rows && col < g.width;
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (in) {
+                        const float *p = stage + r * S::kStagingPitch + staged;
+                        v = *reinterpret_cast<const float4 *>(p);
+                        if (SWIGLU) {
+                            const float4 u = *reinterpret_cast<const float4 *>(p + 32);
+                            v = make_float4(silu(v.x) * u.x, silu(v.y) * u.y, silu(v.z) * u.z, silu(v.w) * u.w);
+                        }
+                    }
+                    const int64_t o = (int64_t)(T.row0 + r) * g.width + col;
+                    if (OUT == PMOE_TYPE_F32) {
+                        if (in)
+                            *reinterpret_cast<float4 *>(static_cast<float *>(g.out) + o) = v;
+                    } else if (OUT == PMOE_TYPE_BF16) {
+                        if (in)
+                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.out) + o) =
+                                make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+                    } else { // 8 lanes have a block
+                        const uint32_t byte = q8::scale_byte(q8::top_of_8_lanes(q8::top4(v.x, v.y, v.z, v.w)));
+                        if (in) {
+                            *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(g.out) + o) =
+                                q8::codes4(v.x, v.y, v.z, v.w, byte);
+                            if (lane % 8 == 0)
+                                g.out_scales[o / 32] = (uint8_t)byte;
+                        }
+                    }
+                }
+                epilogue_sync();
+            }
+        }
     } else {
         // ---- epilogue, 64 accumulator columns at a time: 64 output columns, or 32 of a SwiGLU
         constexpr int kChunks = NT / 64, kHalves = SWIGLU ? 1 : 2; // halves: 32 output columns
@@ -731,18 +824,8 @@ pmoe_status launch(const Maps &m, const Grouped &g, int64_t tiles, cudaStream_t 
             ready.fetch_or(1ull << dev);
     }
     constexpr int kCtas = PAIR ? 2 : 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles < kNumSMs / kCtas ? tiles * kCtas : kNumSMs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::smem(g.E);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCtas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, m.x, m.xwide, m.w, g));
+    const unsigned grid = (unsigned)(tiles < kNumSMs / kCtas ? tiles * kCtas : kNumSMs);
+    return launch_early(kernel, dim3(grid), kThreads, S::smem(g.E), st, kCtas, m.x, m.xwide, m.w, g);
 }
 
 template <bool Q8IN, bool PAIR, int ROWS, int NT>

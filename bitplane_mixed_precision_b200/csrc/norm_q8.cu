@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 
 #include "common.h"
+#include "pipe.cuh"
 #include "q8.cuh"
 
 namespace pmoe {
@@ -30,6 +31,8 @@ __global__ void __launch_bounds__(kMaxNormThreads)
     const int64_t row = (int64_t)blockIdx.x * H;
     float4 v[V];
     float ss = 0.0f;
+    pipe::launch_dependents();
+    pipe::wait_prerequisites();
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int i = tid + j * blockDim.x;
@@ -96,6 +99,8 @@ __global__ void __launch_bounds__(256) quantize_q8_kernel(const void *__restrict
                                                           uint8_t *__restrict__ codes, uint8_t *__restrict__ scales)
 {
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    pipe::launch_dependents();
+    pipe::wait_prerequisites();
     for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x; i0 < n4; i0 += step) { // the whole block takes every step
         const int64_t i = i0 + threadIdx.x;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -136,11 +141,8 @@ pmoe_status pmoe_quantize_q8(const void *w, int w_is_bf16, int64_t rows, int K, 
     const int64_t n4 = rows * K / 4;
     const int64_t blocks = (n4 + 255) / 256;
     const int grid = (int)(blocks < 16 * kNumSMs ? blocks : 16 * kNumSMs);
-    if (w_is_bf16)
-        quantize_q8_kernel<true><<<grid, 256, 0, (cudaStream_t)stream>>>(w, n4, codes, scales);
-    else
-        quantize_q8_kernel<false><<<grid, 256, 0, (cudaStream_t)stream>>>(w, n4, codes, scales);
-    return launch_status();
+    return launch_early(w_is_bf16 ? quantize_q8_kernel<true> : quantize_q8_kernel<false>, dim3(grid), 256, 0,
+                        (cudaStream_t)stream, 1, w, n4, codes, scales);
 }
 
 pmoe_status pmoe_residual_norm_q8(float *r, const float *y, const float *gain, float eps, int T, int H, uint8_t *codes,
@@ -162,22 +164,11 @@ pmoe_status pmoe_residual_norm_q8(float *r, const float *y, const float *gain, f
     while (n4 > V * kMaxNormThreads)
         V *= 2;
     const int threads = ((n4 + V - 1) / V + 31) / 32 * 32;
-    const cudaStream_t st = (cudaStream_t)stream;
-    switch (V) {
-    case 1:
-        residual_norm_q8_kernel<1><<<T, threads, 0, st>>>(r, y, gain, eps, H, codes, scales, x);
-        break;
-    case 2:
-        residual_norm_q8_kernel<2><<<T, threads, 0, st>>>(r, y, gain, eps, H, codes, scales, x);
-        break;
-    case 4:
-        residual_norm_q8_kernel<4><<<T, threads, 0, st>>>(r, y, gain, eps, H, codes, scales, x);
-        break;
-    default:
-        residual_norm_q8_kernel<8><<<T, threads, 0, st>>>(r, y, gain, eps, H, codes, scales, x);
-        break;
-    }
-    return launch_status();
+    auto *kernel = V == 1   ? residual_norm_q8_kernel<1>
+                   : V == 2 ? residual_norm_q8_kernel<2>
+                   : V == 4 ? residual_norm_q8_kernel<4>
+                            : residual_norm_q8_kernel<8>;
+    return launch_early(kernel, dim3(T), threads, 0, (cudaStream_t)stream, 1, r, y, gain, eps, H, codes, scales, x);
 }
 
 } // extern "C"
