@@ -148,9 +148,15 @@ def _ptr(x):
 def _dense_ptr(x):
     """_ptr of a tensor or array whose elements lie one after another (views with gaps are refused:
     the C ABI takes no strides)."""
-    if hasattr(x, "is_contiguous") and not x.is_contiguous():
+    if x is None or type(x) is int:
+        return x
+    try:
+        dense = x.is_contiguous()
+    except AttributeError:
+        return _ptr(x)
+    if not dense:
         raise ValueError("tensor arguments must be contiguous")
-    return _ptr(x)
+    return x.data_ptr()
 
 
 def _stream(s):

@@ -157,9 +157,11 @@ pmoe_status pmoe_residual_norm_q8(float *r, const float *y, const float *gain, f
     if (T == 0)
         return PMOE_OK;
     PMOE_TRY(on_current_device({r, y, gain, codes, scales, x}));
+    // 512 threads a row where it is long enough: at 4096 x 4096, 38.8 us (5.6 TB/s) against 40.6 with 256 threads
+    // (their 3.5 rounds of blocks end in half a round), 43.1 with 1024 and 49.1 with 128.
     const int n4 = H / 4;
     int V = 1;
-    while (V < 8 && n4 > V * 256)
+    while (V < 8 && n4 > V * 512)
         V *= 2;
     while (n4 > V * kMaxNormThreads)
         V *= 2;
