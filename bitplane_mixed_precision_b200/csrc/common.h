@@ -25,24 +25,20 @@ inline pmoe_status launch_status() { return cuda_status(cudaGetLastError()); }
 
 // Launches a kernel that may start before the launch in front of it on the stream has finished, up to its
 // pipe::wait_prerequisites(): its setup then overlaps that one's end. Every such kernel calls that before it touches
-// global memory. ctas: cluster size (1: none).
+// global memory.
 template <class... P, class... A>
-pmoe_status launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int ctas,
-                         const A &...args)
+pmoe_status launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    cfg.numAttrs = 1;
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...));
 }
 

@@ -268,9 +268,9 @@ pmoe_status pmoe_group_pairs(const int32_t *ids, int T, int k, int E, int32_t *o
                                        (int)smem));
     int32_t *hist = blocks > 1 ? static_cast<int32_t *>(ws) : nullptr;
     if (hist)
-        PMOE_TRY(launch_early(group_histogram_kernel, dim3(blocks), kGroupThreads, E * sizeof(int32_t), st, 1, ids, (int)P,
+        PMOE_TRY(launch_early(group_histogram_kernel, dim3(blocks), kGroupThreads, E * sizeof(int32_t), st, ids, (int)P,
                               E, chunk, hist));
-    return launch_early(group_scatter_kernel, dim3(blocks), kGroupThreads, smem, st, 1, ids, (int)P, k, E, chunk, hist,
+    return launch_early(group_scatter_kernel, dim3(blocks), kGroupThreads, smem, st, ids, (int)P, k, E, chunk, hist,
                         offsets, row_of, token_of);
 }
 
@@ -288,7 +288,7 @@ pmoe_status pmoe_combine_rows(const void *rows, int rows_are_bf16, const int32_t
         return PMOE_OK;
     PMOE_TRY(on_current_device({rows, row_of, w, y}));
     return launch_early(rows_are_bf16 ? combine_rows_kernel<true> : combine_rows_kernel<false>, dim3(T * chunks), 128, 0,
-                        (cudaStream_t)stream, 1, rows, row_of, w, (int)P, k, H, chunks, y);
+                        (cudaStream_t)stream, rows, row_of, w, (int)P, k, H, chunks, y);
 }
 
 } // extern "C"

@@ -7,24 +7,23 @@
 // other way round, with N following the number of rows, cost 20 to 50 % more at 40 and 320 rows an expert, and
 // bound single rows by the MMAs.) For SwiGLU the NT rows alternate between 32 gate rows and the up rows of the same
 // columns of h, so that one thread has both.
-// An SM takes in about 64 bytes per cycle, which bounds a 128 x 256 tile at 768 cycles per stage against 512 of
-// MMAs. With many rows per expert two neighbouring SMs (PAIR) therefore share a tile of 256 x 256: each brings its
-// 128 rows of x and half of the matrix rows, the MMAs that the first one's thread issues multiply in both, and each
-// has the accumulators of its own rows.
-// A persistent CTA (or pair) takes tiles at a stride of all of them: every role finds a tile's expert in a prefix
+// An SM takes in about 64 bytes per cycle: 48 KB take longer than the stage's MMAs (768 against 512 cycles at least),
+// which is what bounds long prompts. (Pairs of SMs sharing 256 x 256 tiles, 32 KB per SM and stage, gained 6 to 8 %
+// where experts have multiples of 256 rows and nothing on average over ragged ones.)
+// A persistent CTA per SM takes tiles at a stride of all of them: every role finds a tile's expert in a prefix
 // table of row tiles that the CTA makes from `offsets` when it starts. Roles, one warp each unless said otherwise:
-//   - producer: tiled TMA loads of 128 bytes of k per row into a ring of stages: the matrix rows
-//     and rows of x that follow one another by few and large boxes (the SM's TMA unit is busy for 85 cycles or more
-//     per instruction, whatever its size);
+//   - producer: tiled TMA loads of 128 bytes of k per row into a ring of stages: the matrix rows and rows of x that
+//     follow one another by few and large boxes (the SM's TMA unit is busy for 85 cycles or more per instruction,
+//     whatever its size);
 //   - four warps gather the rows of x of an index with 16-byte asynchronous copies, 8 lanes a row, in the layout
 //     that TMA writes. (Gathering TMA loads of four rows were tried first: 32 of them per stage took about 2700
 //     cycles to issue, five times the MMAs of a stage.) Rows that no expert has are not loaded;
 //   - q8: two warps bring the scale bytes (one word per row and stage) into the order the tensor cores take, loaded
 //     several stages ahead;
-//   - MMA: one thread, which waits for one barrier per stage (a second wait and a fence of its own per stage cost
-//     the q8 products 10 to 20 %: everybody else fences and arrives on that one barrier); four K slices per stage, accumulators in tensor memory: two of NT columns. q8 needs tensor
-//     memory for scales too, so its two of 256 share 64 columns: the next tile starts once the epilogue has read
-//     those, which it does first;
+//   - MMA: one thread, which waits for one barrier per stage (a second wait and a fence of its own per stage cost the
+//     q8 products 10 to 20 %: everybody else fences and arrives on that one barrier); four K slices per stage,
+//     accumulators in tensor memory: two of NT columns. q8 needs tensor memory for scales too, so its two of 256 share
+//     64 columns: the next tile starts once the epilogue has read those, which it does first;
 //   - epilogue, four warps (one per quarter of the tensor-memory lanes = 32 rows): SwiGLU and the rounding on
 //     registers (a thread has 32 neighbouring columns of one row: a whole q8 block), then through shared memory so
 //     that rows are stored in pieces of 128 bytes.
@@ -67,15 +66,12 @@ struct Grouped {
 
 constexpr int kMostStages = 12;
 
-template <bool Q8IN, bool PAIR, int ROWS, int NT> struct Shape {
-    static_assert(!PAIR || (ROWS == 128 && NT == 256), "shapes");
-    static constexpr bool kPair = PAIR;
-    static constexpr int kBRows = PAIR ? NT / 2 : NT; // matrix rows in this CTA's stages
-    static constexpr int kA = ROWS * kRowBytes, kB = kBRows * kRowBytes;
-    static constexpr int kAtoms = NT / 128; // scale blocks of 128 matrix rows (a pair's CTAs have all of them)
+template <bool Q8IN, int ROWS, int NT> struct Shape {
+    static constexpr int kA = ROWS * kRowBytes, kB = NT * kRowBytes;
+    static constexpr int kAtoms = NT / 128; // scale blocks of 128 matrix rows
     static constexpr int kScales = Q8IN ? 512 * (1 + kAtoms) : 0;
-    static constexpr int kStaging = ROWS == 32 ? 32 * 132 * 4 : 4 * 32 * kStageRowBytes;
     static constexpr int kStagingPitch = 132; // ROWS = 32: floats of a staged row of 128 columns
+    static constexpr int kStaging = ROWS == 32 ? 32 * kStagingPitch * 4 : 4 * 32 * kStageRowBytes;
     // the MMA reads 128 rows from a stage's rows of x even when it has 32 (the lanes of the others are not used):
     // what follows has to be there
     static constexpr int kPad = (kLanes - ROWS) * kRowBytes > kB ? (kLanes - ROWS) * kRowBytes - kB : 0;
@@ -102,7 +98,7 @@ template <bool Q8IN, bool PAIR, int ROWS, int NT> struct Shape {
 };
 
 struct Bars {
-    uint64_t full[kMostStages]; // a stage is complete (of a pair: in both CTAs, on the first one's barrier)
+    uint64_t full[kMostStages]; // a stage is complete
     uint64_t empty[kMostStages];
     uint64_t acc_full[2], acc_free[2], done;
     uint32_t tmem;
@@ -110,33 +106,6 @@ struct Bars {
     int part[kThreads / 32];
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
-
-// ---- the other CTA of a pair
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The same place in the cluster's first CTA.
-__device__ __forceinline__ uint32_t in_first(const void *p)
-{
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(pipe::smem_u32(p)));
-    return a;
-}
-
-__device__ __forceinline__ void arrive_in_first(uint64_t *bar)
-{
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
-}
 
 // A wait that gives up after limit_ns, or as soon as another role has given up.
 struct Waiter {
@@ -240,12 +209,6 @@ template <int ROWS> struct Walk {
     }
 };
 
-// Rows that the second CTA of a pair has of the tile whose first part is T.
-__device__ __forceinline__ int pair_rows(const Tile &T, const Grouped &g)
-{
-    return T.rows < 128 ? 0 : max(0, min(128, expert_rows(g, T.e).y - T.row0 - 128));
-}
-
 // Prefix sums of the experts' row tiles, first[0..E]; all threads.
 template <int ROWS> __device__ void row_tiles(const Grouped &g, int *first, int *part)
 {
@@ -307,19 +270,11 @@ __device__ __forceinline__ bool epilogue_all(bool ok)
     return r != 0;
 }
 
-// A warp's part of a stage is there (fenced for the tensor cores).
-template <class S> __device__ __forceinline__ void arrive_full(Bars *bars, int s)
-{
-    if (S::kPair)
-        arrive_in_first(&bars->full[s]);
-    else
-        pipe::mbar_arrive(&bars->full[s]);
-}
-
 // The scale warps: 32 * ROWS rows, a lane has rows lane + 32 j. The words of four stages (16 bytes of a row) are
-// loaded together, DEPTH such groups ahead of their use. rows_of(T, j) is the row's scale bytes, or NULL where
+// loaded together, while those of the four before are handed over. (Two or three such groups ahead, or a loop
+// unrolled over them, were 1 to 8 % slower.) rows_of(T, j) is the row's scale bytes, or NULL where
 // the values are zeros or not used (scale 1, so that zeros stay zeros).
-template <class S, int ROWS, int DEPTH, class RowsOf, class Tiles>
+template <class S, int ROWS, class RowsOf, class Tiles>
 __device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const Waiter &wait, uint8_t *dst, int tiles,
                                            int t0, int step, int where, const RowsOf &rows_of, Tiles tile)
 {
@@ -328,9 +283,9 @@ __device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const W
     const bool wide = g.iters % 4 == 0; // rows of scales are 16-byte aligned
     constexpr uint32_t kOnes = 0x7f7f7f7fu;
     const uint8_t *row[ROWS];
-    uint4 next[DEPTH][ROWS];
+    uint4 next[ROWS];
     int at = t0, group = 0; // the next group to load
-    auto load = [&](uint4(&v)[ROWS]) {
+    auto load = [&] {
         if (at >= tiles)
             return;
         if (group == 0) {
@@ -341,17 +296,17 @@ __device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const W
         }
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            v[j] = make_uint4(kOnes, kOnes, kOnes, kOnes);
+            next[j] = make_uint4(kOnes, kOnes, kOnes, kOnes);
             if (row[j]) {
                 const uint32_t *p = reinterpret_cast<const uint32_t *>(row[j]) + 4 * group;
                 if (wide) {
-                    v[j] = __ldg(reinterpret_cast<const uint4 *>(p));
+                    next[j] = __ldg(reinterpret_cast<const uint4 *>(p));
                 } else {
                     const int left = g.iters - 4 * group;
-                    v[j].x = __ldg(p);
-                    v[j].y = left > 1 ? __ldg(p + 1) : kOnes;
-                    v[j].z = left > 2 ? __ldg(p + 2) : kOnes;
-                    v[j].w = left > 3 ? __ldg(p + 3) : kOnes;
+                    next[j].x = __ldg(p);
+                    next[j].y = left > 1 ? __ldg(p + 1) : kOnes;
+                    next[j].z = left > 2 ? __ldg(p + 2) : kOnes;
+                    next[j].w = left > 3 ? __ldg(p + 3) : kOnes;
                 }
             }
         }
@@ -360,21 +315,15 @@ __device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const W
             at += step;
         }
     };
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-        load(next[d]);
+    load();
     Ring<S::kStages> ring;
     for (int t = t0; t < tiles; t += step) {
         for (int k = 0; k < g.iters; k += 4) {
             uint4 now[ROWS];
 #pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                now[j] = next[0][j];
-#pragma unroll
-                for (int d = 1; d < DEPTH; ++d)
-                    next[d - 1][j] = next[d][j];
-            }
-            load(next[DEPTH - 1]);
+            for (int j = 0; j < ROWS; ++j)
+                now[j] = next[j];
+            load();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (k + q >= g.iters)
@@ -391,39 +340,38 @@ __device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const W
                 umma::fence_smem_async();
                 __syncwarp();
                 if (lane == 0)
-                    arrive_full<S>(bars, ring.s);
+                    pipe::mbar_arrive(&bars->full[ring.s]);
                 ring.next();
             }
         }
     }
 }
 
-template <bool Q8IN, bool SWIGLU, bool PAIR, int ROWS, int NT, int OUT>
+template <bool Q8IN, bool SWIGLU, int ROWS, int NT, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xwide,
                    const __grid_constant__ CUtensorMap wmap, const __grid_constant__ Grouped g)
 {
-    using S = Shape<Q8IN, PAIR, ROWS, NT>;
+    using S = Shape<Q8IN, ROWS, NT>;
     constexpr int kCols = SWIGLU ? NT / 2 : NT; // output columns of a tile
-    constexpr int kElem = Q8IN ? 1 : 2, kCtas = PAIR ? 2 : 1;
+    constexpr int kElem = Q8IN ? 1 : 2;
     constexpr int kBoxRows = SWIGLU ? 64 : 128, kBoxCols = SWIGLU ? 32 : 128; // a box of matrix rows, its columns
-    constexpr int kBoxes = S::kBRows / kBoxRows;
+    constexpr int kBoxes = NT / kBoxRows;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (pipe::smem_u32(raw) & 1023)) & 1023);
     Bars *bars = reinterpret_cast<Bars *>(smem + S::kBarAt);
     int *first = reinterpret_cast<int *>(smem + S::kTableAt);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = PAIR ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            // the producer with its bytes; of each CTA, two scale warps and the gather warps
-            pipe::mbar_init(&bars->full[s], 1 + kCtas * ((Q8IN ? 2 : 0) + (g.index ? kGatherWarps : 0)));
+            // the producer with its bytes, two scale warps, the gather warps
+            pipe::mbar_init(&bars->full[s], 1 + (Q8IN ? 2 : 0) + (g.index ? kGatherWarps : 0));
             pipe::mbar_init(&bars->empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             pipe::mbar_init(&bars->acc_full[i], 1);
-            pipe::mbar_init(&bars->acc_free[i], 4 * kCtas);
+            pipe::mbar_init(&bars->acc_free[i], 4);
         }
         pipe::mbar_init(&bars->done, 1);
         bars->abort = 0;
@@ -431,63 +379,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma::prefetch_map(&xmap);
         tma::prefetch_map(&wmap);
     }
-    if (warp == 1)
-        umma::tmem_alloc_group<kCtas>(&bars->tmem, S::kTmemCols);
+    if (warp == 1) {
+        umma::tmem_alloc(&bars->tmem, S::kTmemCols);
+        umma::tmem_relinquish();
+    }
     pipe::launch_dependents();
     pipe::wait_prerequisites(); // nothing of another launch is read or written before this
     umma::fence_before_sync();
-    row_tiles<kCtas * ROWS>(g, first, bars->part); // ends with the block's barrier
-    if (PAIR)
-        cluster_sync(); // the other CTA's barriers are there
+    row_tiles<ROWS>(g, first, bars->part); // ends with the block's barrier
     umma::fence_after_sync();
     const uint32_t tmem = bars->tmem;
-    const int tiles = first[g.E] * g.ntiles, t0 = blockIdx.x / kCtas, step = gridDim.x / kCtas;
+    const int tiles = first[g.E] * g.ntiles, t0 = blockIdx.x, step = gridDim.x;
     const Waiter wait{bars, g.limit_ns};
-    Walk<kCtas * ROWS> walk(g, first, kCols);
-    auto tile = [walk, rank](int t) mutable { // this CTA's rows of a pair's tile (perhaps none)
-        Tile T = walk(t);
-        if (PAIR) {
-            T.row0 += rank * ROWS;
-            T.rows = max(0, min(ROWS, T.rows - rank * ROWS));
-        }
-        return T;
-    };
+    Walk<ROWS> tile(g, first, kCols);
 
     if (warp == 0) {
-        // ---- producer. A pair's loads complete on the first CTA's barriers.
+        // ---- producer
         Ring<S::kStages> ring;
         for (int t = t0; t < tiles; t += step) {
             const Tile T = tile(t);
             const bool one = ROWS == 128 && T.rows > 64; // one box of 128 rows
             const int loads = g.index ? 0 : one ? 1 : (T.rows + 31) / 32;
-            uint32_t bytes = (uint32_t)(loads * (one ? 128 : 32) * kRowBytes + S::kB);
-            if (PAIR && rank == 0) { // and the second CTA's
-                const int rows = pair_rows(T, g);
-                bytes += (uint32_t)(g.index ? 0 : rows > 64 ? 128 : (rows + 31) / 32 * 32) * kRowBytes + S::kB;
-            }
+            const uint32_t bytes = (uint32_t)(loads * (one ? 128 : 32) * kRowBytes + S::kB);
             for (int i = 0; i < g.iters; ++i, ring.next()) {
                 const int s = ring.s;
                 if (!ring.free(wait, bars, 1))
                     goto produced;
                 uint8_t *a = smem + s * (S::kA + S::kB), *b = a + S::kA;
                 const int x = i * (kRowBytes / kElem);
-                if (lane == 0 && rank == 0)
+                if (lane == 0)
                     pipe::mbar_arrive_expect_tx(&bars->full[s], bytes);
                 __syncwarp();
-                const uint32_t full = PAIR ? in_first(&bars->full[s]) : pipe::smem_u32(&bars->full[s]);
                 if (lane < kBoxes)
-                    tma::load_4d<kCtas>(b + lane * kBoxRows * kRowBytes, &wmap, x,
-                                        T.col0 + (rank * kBoxes + lane) * kBoxCols, 0, T.e, full);
+                    tma::load_4d(b + lane * kBoxRows * kRowBytes, &wmap, x, T.col0 + lane * kBoxCols, 0, T.e,
+                                 &bars->full[s]);
                 else if (lane < kBoxes + loads)
-                    tma::load_2d<kCtas>(a + (lane - kBoxes) * 32 * kRowBytes, one ? &xwide : &xmap, x,
-                                        T.row0 + 32 * (lane - kBoxes), full);
+                    tma::load_2d(a + (lane - kBoxes) * 32 * kRowBytes, one ? &xwide : &xmap, x,
+                                 T.row0 + 32 * (lane - kBoxes), &bars->full[s]);
             }
         }
     produced:
         __syncwarp();
     } else if (warp == 1) {
-        // ---- MMA (of a pair, the first CTA's)
-        if (lane == 0 && rank == 0) {
+        // ---- MMA
+        if (lane == 0) {
             Ring<S::kStages> ring;
             const uint64_t a0 = umma::smem_desc_sw128(smem), b0 = umma::smem_desc_sw128(smem + S::kA);
             bool ok = true;
@@ -512,32 +447,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t sa = tmem + S::kScaleCols + 4 * s;
                         const uint32_t sb = tmem + S::kScaleCols + 4 * S::kSets + 4 * S::kAtoms * s;
                         const uint8_t *sc = smem + S::kScalesAt + s * S::kScales;
-                        umma::copy_scales<kCtas>(sa, sc);
+                        umma::copy_scales(sa, sc);
                         for (int j = 0; j < S::kAtoms; ++j)
-                            umma::copy_scales<kCtas>(sb + 4 * j, sc + 512 * (j + 1));
+                            umma::copy_scales(sb + 4 * j, sc + 512 * (j + 1));
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            umma::mma_mxf8<kCtas>(d, ad + 2 * j, bd + 2 * j, umma::idesc_mxf8(kCtas * kLanes, NT, j), sa,
-                                                  sb, (k | j) != 0);
+                            umma::mma_mxf8(d, ad + 2 * j, bd + 2 * j, umma::idesc_mxf8(kLanes, NT, j), sa, sb,
+                                           (k | j) != 0);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            umma::mma_bf16<kCtas>(d, ad + 2 * j, bd + 2 * j, umma::idesc_bf16(kCtas * kLanes, NT),
-                                                  (k | j) != 0);
+                            umma::mma_f16(d, ad + 2 * j, bd + 2 * j, umma::idesc_bf16(kLanes, NT), (k | j) != 0);
                     }
-                    umma::commit_group<kCtas>(&bars->empty[s]);
+                    umma::commit(&bars->empty[s]);
                 }
                 if (ok)
-                    umma::commit_group<kCtas>(&bars->acc_full[i & 1]);
+                    umma::commit(&bars->acc_full[i & 1]);
             }
-            umma::commit_local<kCtas>(&bars->done);
+            umma::commit(&bars->done);
             drain(&bars->done, 0);
         }
         __syncwarp();
     } else if (warp == 2) {
         // ---- scale bytes of the rows of x
         if (Q8IN)
-            scale_warp<S, ROWS / 32, 3>(
+            scale_warp<S, ROWS / 32>(
                 g, bars, wait, smem + S::kScalesAt, tiles, t0, step, 6,
                 [&](const Tile &T, int r) -> const uint8_t * {
                     if (r >= T.rows)
@@ -550,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 3) {
         // ---- scale bytes of the matrix rows
         if (Q8IN)
-            scale_warp<S, NT / 32, NT == 256 ? 2 : 3>(
+            scale_warp<S, NT / 32>(
                 g, bars, wait, smem + S::kScalesAt + 512, tiles, t0, step, 7,
                 [&](const Tile &T, int r) -> const uint8_t * {
                     const bool up = SWIGLU && (r & 32);
@@ -573,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma::fence_smem_async();
                 __syncwarp();
                 if (lane == 0)
-                    arrive_full<S>(bars, behind.s);
+                    pipe::mbar_arrive(&bars->full[behind.s]);
                 behind.next();
                 --ahead;
             };
@@ -715,12 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j == (S::kOverlap ? 0 : kChunks - 1)) {
                     umma::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR)
-                            arrive_in_first(&bars->acc_free[i & 1]);
-                        else
-                            pipe::mbar_arrive(&bars->acc_free[i & 1]);
-                    }
+                    if (lane == 0)
+                        pipe::mbar_arrive(&bars->acc_free[i & 1]);
                 }
                 if (!any)
                     continue;
@@ -795,13 +725,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     __syncwarp();
     umma::fence_before_sync();
-    if (PAIR)
-        cluster_sync(); // neither CTA's shared or tensor memory goes while the other uses it
-    else
-        __syncthreads();
+    __syncthreads();
     if (warp == 1) {
         umma::fence_after_sync();
-        umma::tmem_dealloc_group<kCtas>(tmem, S::kTmemCols);
+        umma::tmem_dealloc(tmem, S::kTmemCols);
     }
 }
 
@@ -809,11 +736,11 @@ struct Maps {
     CUtensorMap x, xwide, w;
 };
 
-template <bool Q8IN, bool SWIGLU, bool PAIR, int ROWS, int NT, int OUT>
+template <bool Q8IN, bool SWIGLU, int ROWS, int NT, int OUT>
 pmoe_status launch(const Maps &m, const Grouped &g, int64_t tiles, cudaStream_t st)
 {
-    using S = Shape<Q8IN, PAIR, ROWS, NT>;
-    auto *kernel = grouped_kernel<Q8IN, SWIGLU, PAIR, ROWS, NT, OUT>;
+    using S = Shape<Q8IN, ROWS, NT>;
+    auto *kernel = grouped_kernel<Q8IN, SWIGLU, ROWS, NT, OUT>;
     static std::atomic<uint64_t> ready{0}; // devices whose shared-memory limit of this kernel is set
     int dev = 0;
     PMOE_CUDA(cudaGetDevice(&dev));
@@ -823,38 +750,30 @@ pmoe_status launch(const Maps &m, const Grouped &g, int64_t tiles, cudaStream_t 
         if (dev < 64)
             ready.fetch_or(1ull << dev);
     }
-    constexpr int kCtas = PAIR ? 2 : 1;
-    const unsigned grid = (unsigned)(tiles < kNumSMs / kCtas ? tiles * kCtas : kNumSMs);
-    return launch_early(kernel, dim3(grid), kThreads, S::smem(g.E), st, kCtas, m.x, m.xwide, m.w, g);
+    return launch_early(kernel, dim3((unsigned)(tiles < kNumSMs ? tiles : kNumSMs)), kThreads, S::smem(g.E), st, m.x,
+                        m.xwide, m.w, g);
 }
 
-template <bool Q8IN, bool PAIR, int ROWS, int NT>
+template <bool Q8IN, int ROWS, int NT>
 pmoe_status launch_out(bool swiglu, int out_type, const Maps &m, const Grouped &g, int64_t tiles, cudaStream_t st)
 {
     if (swiglu)
-        return out_type == PMOE_TYPE_Q8 ? launch<Q8IN, true, PAIR, ROWS, NT, PMOE_TYPE_Q8>(m, g, tiles, st)
-                                        : launch<Q8IN, true, PAIR, ROWS, NT, PMOE_TYPE_BF16>(m, g, tiles, st);
-    return out_type == PMOE_TYPE_F32 ? launch<Q8IN, false, PAIR, ROWS, NT, PMOE_TYPE_F32>(m, g, tiles, st)
-                                     : launch<Q8IN, false, PAIR, ROWS, NT, PMOE_TYPE_BF16>(m, g, tiles, st);
+        return out_type == PMOE_TYPE_Q8 ? launch<Q8IN, true, ROWS, NT, PMOE_TYPE_Q8>(m, g, tiles, st)
+                                        : launch<Q8IN, true, ROWS, NT, PMOE_TYPE_BF16>(m, g, tiles, st);
+    return out_type == PMOE_TYPE_F32 ? launch<Q8IN, false, ROWS, NT, PMOE_TYPE_F32>(m, g, tiles, st)
+                                     : launch<Q8IN, false, ROWS, NT, PMOE_TYPE_BF16>(m, g, tiles, st);
 }
 
 template <bool Q8IN>
 pmoe_status launch_shape(int tile_rows, int nt, bool swiglu, int out_type, const Maps &m, const Grouped &g,
                          int64_t tiles, cudaStream_t st)
 {
-    if (tile_rows == 256)
-        return launch_out<Q8IN, true, 128, 256>(swiglu, out_type, m, g, tiles, st);
     if (tile_rows == 32)
-        return nt == 128 ? launch_out<Q8IN, false, 32, 128>(swiglu, out_type, m, g, tiles, st)
-                         : launch_out<Q8IN, false, 32, 256>(swiglu, out_type, m, g, tiles, st);
-    return nt == 128 ? launch_out<Q8IN, false, 128, 128>(swiglu, out_type, m, g, tiles, st)
-                     : launch_out<Q8IN, false, 128, 256>(swiglu, out_type, m, g, tiles, st);
+        return nt == 128 ? launch_out<Q8IN, 32, 128>(swiglu, out_type, m, g, tiles, st)
+                         : launch_out<Q8IN, 32, 256>(swiglu, out_type, m, g, tiles, st);
+    return nt == 128 ? launch_out<Q8IN, 128, 128>(swiglu, out_type, m, g, tiles, st)
+                     : launch_out<Q8IN, 128, 256>(swiglu, out_type, m, g, tiles, st);
 }
-
-// Rows per expert from which a pair's tiles of 256 rows are faster than single tiles of 128: a stage of the pair
-// takes 0.92 of a single one's time (bf16 1391 against 1292 TFLOP/s, q8 2236 against 2162, at 1024 rows an
-// expert), but an expert's last tile wastes 128 rows on average instead of 64.
-constexpr int kPairRows = 700;
 
 pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offsets, int rows, int out_type, void *out,
                     uint8_t *out_scales, bool swiglu, pmoe_stream stream)
@@ -882,13 +801,15 @@ pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offs
         return PMOE_OK;
     PMOE_TRY(on_current_device({W->w, W->scales, X->x, X->scales, X->index, offsets, out, out_scales}));
 
-    // Rows of x per tile by the rows an expert has on average; matrix rows per tile by whether 256 give half of
-    // the SMs a tile.
+    // Rows of x per tile by the rows an expert has on average: at 16, tiles of 32 against 128 took 181 against 176 us
+    // (q8, 256 experts of 4096 x 1024), 177 against 187 (q8 SwiGLU), 333 against 339 (bf16); at 32, 227 against 182 and
+    // 386 against 352. Matrix rows per tile by whether 256 give half of the SMs a tile: one row for each of 9 experts,
+    // 2048 x 4096, 18.4 us with 128 against 19.5 (72 tiles), of 10 experts 29.0 against 21.6 (80 tiles).
     const int hit = W->E < rows ? W->E : rows;
-    const int tile_rows = rows <= 16 * (int64_t)hit ? 32 : rows < kPairRows * (int64_t)hit ? 128 : 256;
+    const int tile_rows = rows <= 16 * (int64_t)hit ? 32 : 128;
     const int64_t most = (int64_t)rows / tile_rows + hit; // at most one ragged row tile per expert
     const int wide = swiglu ? 128 : 256;
-    const int nt = tile_rows < 256 && most * ((width + wide - 1) / wide) < kNumSMs / 2 ? 128 : 256;
+    const int nt = most * ((width + wide - 1) / wide) < kNumSMs / 2 ? 128 : 256;
     const int cols = swiglu ? nt / 2 : nt;
     const int ntiles = (width + cols - 1) / cols;
     // offsets that overlap could name every row for every expert: even those tiles are counted in an int

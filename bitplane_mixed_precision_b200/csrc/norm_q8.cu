@@ -142,7 +142,7 @@ pmoe_status pmoe_quantize_q8(const void *w, int w_is_bf16, int64_t rows, int K, 
     const int64_t blocks = (n4 + 255) / 256;
     const int grid = (int)(blocks < 16 * kNumSMs ? blocks : 16 * kNumSMs);
     return launch_early(w_is_bf16 ? quantize_q8_kernel<true> : quantize_q8_kernel<false>, dim3(grid), 256, 0,
-                        (cudaStream_t)stream, 1, w, n4, codes, scales);
+                        (cudaStream_t)stream, w, n4, codes, scales);
 }
 
 pmoe_status pmoe_residual_norm_q8(float *r, const float *y, const float *gain, float eps, int T, int H, uint8_t *codes,
@@ -170,7 +170,7 @@ pmoe_status pmoe_residual_norm_q8(float *r, const float *y, const float *gain, f
                    : V == 2 ? residual_norm_q8_kernel<2>
                    : V == 4 ? residual_norm_q8_kernel<4>
                             : residual_norm_q8_kernel<8>;
-    return launch_early(kernel, dim3(T), threads, 0, (cudaStream_t)stream, 1, r, y, gain, eps, H, codes, scales, x);
+    return launch_early(kernel, dim3(T), threads, 0, (cudaStream_t)stream, r, y, gain, eps, H, codes, scales, x);
 }
 
 } // extern "C"

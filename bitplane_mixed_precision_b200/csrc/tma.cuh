@@ -18,15 +18,15 @@ inline pmoe_status make_map(CUtensorMap *map, int elem_bytes, int rank, const vo
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static Encode encode = nullptr;
-    if (!encode) {
+    static const Encode encode = [] {
         void *f = nullptr;
         cudaDriverEntryPointQueryResult found;
-        PMOE_CUDA(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found));
-        if (found != cudaDriverEntryPointSuccess || !f)
-            return cuda_status(cudaErrorNotSupported);
-        encode = reinterpret_cast<Encode>(f);
-    }
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(f) : nullptr;
+    }();
+    if (!encode)
+        return cuda_status(cudaErrorNotSupported);
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     const CUresult r = encode(map, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                               (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, ones,
@@ -40,36 +40,21 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// Loads into this CTA's shared memory, completed in bytes on the barrier at address bar: this CTA's, or with
-// CTAS = 2 (a pair of neighbouring CTAs) one of the pair's first CTA.
-template <int CTAS>
-__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+// Loads into this CTA's shared memory, completed in bytes on bar.
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
 {
-    if (CTAS == 2)
-        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                     "[%0], [%1, {%2, %3}], [%4];" ::"r"(pipe::smem_u32(dst)),
-                     "l"(map), "r"(x), "r"(y), "r"(bar)
-                     : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-                     "%3}], [%4];" ::"r"(pipe::smem_u32(dst)),
-                     "l"(map), "r"(x), "r"(y), "r"(bar)
-                     : "memory");
+    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+                 "[%4];" ::"r"(pipe::smem_u32(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(pipe::smem_u32(bar))
+                 : "memory");
 }
 
-template <int CTAS>
-__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar)
+__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar)
 {
-    if (CTAS == 2)
-        asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                     "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(pipe::smem_u32(dst)),
-                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-                     : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-                     "%3, %4, %5}], [%6];" ::"r"(pipe::smem_u32(dst)),
-                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-                     : "memory");
+    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+                 "%4, %5}], [%6];" ::"r"(pipe::smem_u32(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(pipe::smem_u32(bar))
+                 : "memory");
 }
 
 } // namespace tma

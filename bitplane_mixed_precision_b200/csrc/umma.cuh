@@ -206,68 +206,16 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int j)
            ((uint32_t)j << 29);
 }
 
-// The forms below take the number of CTAs, 1 or 2: with 2, a pair of neighbouring CTAs each have half of A's
-// rows, half of B's rows and the accumulators of their half of A's rows; one thread of the first CTA issues.
-#define PMOE_GROUP_ASM(C, before, after, ...)                                                                          \
-    do {                                                                                                               \
-        if (C == 2)                                                                                                    \
-            asm volatile(before "cta_group::2" after __VA_ARGS__);                                                     \
-        else                                                                                                           \
-            asm volatile(before "cta_group::1" after __VA_ARGS__);                                                     \
-    } while (0)
-
-// One warp of each CTA: allocation of ncols columns (as tmem_alloc), and its release.
-template <int C> __device__ __forceinline__ void tmem_alloc_group(uint32_t *dst, uint32_t ncols)
-{
-    PMOE_GROUP_ASM(C, "tcgen05.alloc.", ".sync.aligned.shared::cta.b32 [%0], %1;", ::"r"(pipe::smem_u32(dst)),
-                   "r"(ncols)
-                   : "memory");
-    PMOE_GROUP_ASM(C, "tcgen05.relinquish_alloc_permit.", ".sync.aligned;", ::: "memory");
-}
-template <int C> __device__ __forceinline__ void tmem_dealloc_group(uint32_t taddr, uint32_t ncols)
-{
-    PMOE_GROUP_ASM(C, "tcgen05.dealloc.", ".sync.aligned.b32 %0, %1;", ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-// D[tmem] (+)= A * B^T, M x N x 16, bf16 or f16 by the instruction descriptor.
-template <int C>
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         bool accumulate)
-{
-    PMOE_GROUP_ASM(C, "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.",
-                   ".kind::f16 [%0], %1, %2, %3, p;\n\t}", ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc),
-                   "r"((uint32_t)accumulate)
-                   : "memory");
-}
-
 // D[tmem] (+)= (A * 2^sa) * (B * 2^sb)^T, M x N x 32, e4m3 inputs, scales in tensor memory.
-template <int C>
 __device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t sa_tmem, uint32_t sb_tmem, bool accumulate)
 {
-    PMOE_GROUP_ASM(C, "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\ttcgen05.mma.",
-                   ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}", ::"r"(d_tmem),
-                   "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"((uint32_t)accumulate)
-                   : "memory");
-}
-
-// An arrival, once the tcgen05 operations this thread issued so far completed, on bar in this CTA, or on the
-// same barrier in each CTA of the pair.
-template <int C> __device__ __forceinline__ void commit_group(uint64_t *bar)
-{
-    if (C == 2)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
-                     "%1;" ::"r"(pipe::smem_u32(bar)),
-                     "h"((uint16_t)3)
-                     : "memory");
-    else
-        commit(bar);
-}
-// The same on bar in this CTA only.
-template <int C> __device__ __forceinline__ void commit_local(uint64_t *bar)
-{
-    PMOE_GROUP_ASM(C, "tcgen05.commit.", ".mbarrier::arrive::one.shared::cluster.b64 [%0];",
-                   ::"r"(pipe::smem_u32(bar)) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %6, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], "
+                 "p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"((uint32_t)accumulate)
+                 : "memory");
 }
 
 // Scale words of 128 rows for the tensor cores: row r at byte (r % 32) * 16 + (r / 32) * 4 of a 512-byte
@@ -275,12 +223,11 @@ template <int C> __device__ __forceinline__ void commit_local(uint64_t *bar)
 // thread issues later see it.
 __host__ __device__ constexpr uint32_t scale_offset(int r) { return (uint32_t)((r % 32) * 16 + (r / 32) * 4); }
 
-// (With a pair, from each CTA's block at the same place to its own tensor memory.)
-template <int C> __device__ __forceinline__ void copy_scales(uint32_t taddr, const void *p)
+__device__ __forceinline__ void copy_scales(uint32_t taddr, const void *p)
 {
     const uint32_t a = pipe::smem_u32(p);
     const uint64_t desc = (uint64_t)((a >> 4) & 0x3fffu) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
-    PMOE_GROUP_ASM(C, "tcgen05.cp.", ".32x128b.warpx4 [%0], %1;", ::"r"(taddr), "l"(desc) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // 64 consecutive fp32 columns of this thread's lane, waited for.

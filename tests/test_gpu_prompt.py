@@ -477,3 +477,20 @@ def test_grouped_wait_that_runs_out_is_reported_and_the_next_call_is_exact(pm, k
     run_matmul(pm, kind, W, X, n, index, off, M, N, K, pm.F32, outs[2])
     assert pm.grouped_error() == (0, 0)
     assert torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("rows", [5, 100])
+def test_grouped_q8_scales_at_both_ends(pm, rows):
+    """Scales far from one that cancel in the products, the smallest scale among them."""
+    K, N = 256, 136
+    g = gen(10)
+    xc, xs = quantize(randn(g, rows, K))
+    wc, ws = quantize(randn(g, 1, N, K))
+    down = torch.randint(0, 20, xs.shape, generator=g, device="cuda").to(torch.uint8)
+    xs = down                                    # 2^-127 .. 2^-108
+    ws = (254 - 20 + torch.randint(0, 20, ws.shape, generator=g, device="cuda")).to(torch.uint8) - 7  # 2^100 .. 2^119
+    x64, w64 = value_of(xc, xs), value_of(wc, ws)
+    o = empty(rows, N, dtype=torch.float32)
+    run_matmul(pm, "q8", (wc, ws), (xc, xs), rows, None, offsets_of([rows]), rows, N, K, pm.F32, o)
+    torch.cuda.synchronize()
+    check_near(o, *products(x64, w64, [rows]), U)
