@@ -17,7 +17,8 @@
 //     whatever its size);
 //   - four warps gather the rows of x of an index with 16-byte asynchronous copies, 8 lanes a row, in the layout
 //     that TMA writes. (Gathering TMA loads of four rows were tried first: 32 of them per stage took about 2700
-//     cycles to issue, five times the MMAs of a stage.) Rows that no expert has are not loaded;
+//     cycles to issue, five times the MMAs of a stage.) Rows that no expert has are not loaded. A fifth warp hands
+//     them over as they land (2 to 4 % faster than the four waiting for copies of their own two stages back);
 //   - q8: two warps bring the scale bytes (one word per row and stage) into the order the tensor cores take, loaded
 //     several stages ahead;
 //   - MMA: one thread, which waits for one barrier per stage (a second wait and a fence of its own per stage cost the
@@ -46,7 +47,7 @@ namespace {
 constexpr int kMaxDenseExperts = 2048;
 constexpr int kRowBytes = 128; // bytes of k per row and stage
 constexpr int kGatherWarps = 4;
-constexpr int kThreads = 256 + 32 * kGatherWarps; // producer, MMA, two scale warps, epilogue (4), gather (4)
+constexpr int kThreads = 256 + 32 * kGatherWarps + 32; // producer, MMA, two scale warps, epilogue (4), gather (4 + 1)
 constexpr int kLanes = 128;                       // the MMA's M
 constexpr int kStageRowBytes = 128;               // epilogue staging: bytes per row
 constexpr uint64_t kDrainNs = 1000ull * 1000 * 1000;
@@ -99,6 +100,7 @@ template <bool Q8IN, int ROWS, int NT> struct Shape {
 
 struct Bars {
     uint64_t full[kMostStages]; // a stage is complete
+    uint64_t gathered[kMostStages]; // its gathered rows have landed
     uint64_t empty[kMostStages];
     uint64_t acc_full[2], acc_free[2], done;
     uint32_t tmem;
@@ -248,6 +250,12 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, int byt
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+// An arrival once all of this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(pipe::smem_u32(bar)) : "memory");
+}
+
 // With the fast exponential and quotient (2 + |g| and 2 units in the last place of a float): far below the
 // rounding of h, and free of branches, so that a thread's columns overlap. (expf and the exact quotient made the
 // epilogue of a 2048-deep q8 tile twice as long as its products.)
@@ -366,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             // the producer with its bytes, two scale warps, the gather warps
-            pipe::mbar_init(&bars->full[s], 1 + (Q8IN ? 2 : 0) + (g.index ? kGatherWarps : 0));
+            pipe::mbar_init(&bars->full[s], 1 + (Q8IN ? 2 : 0) + (g.index ? 1 : 0));
+            pipe::mbar_init(&bars->gathered[s], 32 * kGatherWarps);
             pipe::mbar_init(&bars->empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -493,24 +502,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 },
                 tile);
         __syncwarp();
-    } else if (warp >= 8) {
-        // ---- gathered rows of x: a thread has one 16-byte chunk of rows r0, r0 + 16, ... A stage is handed over
-        // once the copies of two more have been issued.
+    } else if (warp == 8 + kGatherWarps) {
+        // ---- hands gathered rows over: the copies land as other threads' writes, which the tensor cores see behind
+        // this fence
         if (g.index) {
-            constexpr int kLag = 2;
+            Ring<S::kStages> ring;
+            int left = t0 < tiles ? (tiles - t0 + step - 1) / step * g.iters : 0;
+            if (lane == 0)
+                for (; left > 0; --left, ring.next()) {
+                    if (!wait(&bars->gathered[ring.s], ring.phase, 11))
+                        break;
+                    umma::fence_smem_async();
+                    pipe::mbar_arrive(&bars->full[ring.s]);
+                }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // ---- gathered rows of x: a thread has one 16-byte chunk of rows r0, r0 + 16, ...
+        if (g.index) {
             const int r0 = (warp - 8) * 4 + lane / 8, chunk = lane & 7;
             const int64_t pitch = (int64_t)g.K * kElem;
             const uint32_t at = (uint32_t)(r0 * kRowBytes + ((chunk ^ (r0 & 7)) << 4)); // 16 more rows: 2 KB more
-            Ring<S::kStages> ring, behind;
-            int ahead = 0; // stages issued and not handed over
-            auto hand_over = [&] {
-                umma::fence_smem_async();
-                __syncwarp();
-                if (lane == 0)
-                    pipe::mbar_arrive(&bars->full[behind.s]);
-                behind.next();
-                --ahead;
-            };
+            Ring<S::kStages> ring;
             for (int t = t0; t < tiles; t += step) {
                 const Tile T = tile(t);
                 const uint8_t *src[ROWS / 16];
@@ -534,16 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (r0 + 16 * j < T.rows) // rows outside x, and k behind K, are filled with zeros
                             copy16(dst + j * 16 * kRowBytes, src[j] && in ? src[j] + i * kRowBytes : g.x,
                                    src[j] && in ? 16 : 0);
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (++ahead > kLag) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-                        hand_over();
-                    }
+                    copies_arrive(&bars->gathered[ring.s]);
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            while (ahead > 0)
-                hand_over();
         gathered:
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();

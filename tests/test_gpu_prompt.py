@@ -494,3 +494,80 @@ def test_grouped_q8_scales_at_both_ends(pm, rows):
     run_matmul(pm, "q8", (wc, ws), (xc, xs), rows, None, offsets_of([rows]), rows, N, K, pm.F32, o)
     torch.cuda.synchronize()
     check_near(o, *products(x64, w64, [rows]), U)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+def test_grouped_matmul_one_crowded_expert_among_many(pm, kind):
+    """Tiles for few rows, most of them of one expert; as many experts as the products take."""
+    for c in ([0] * 100 + [1000] + [1] * 200, [i % 3 for i in range(2048)]):
+        K, N = 256, 72
+        M = sum(c)
+        W, X, n, index, x64, w64 = case(kind, c, K, N, 77, seed=11)
+        o = empty(M, N, dtype=torch.float32)
+        run_matmul(pm, kind, W, X, n, index, offsets_of(c), M, N, K, pm.F32, o)
+        torch.cuda.synchronize()
+        check_near(o, *products(x64, w64, c), U)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+def test_grouped_matmul_past_2_31_elements(pm, kind):
+    """Rows of out, and rows of x, behind 2^31 elements."""
+    K, N, M = 4096, 4096, 540_000
+    g = gen(12)
+    free = torch.cuda.mem_get_info()[0]
+    if free < 24 << 30:
+        pytest.skip("needs 24 GB")
+    w = randn(g, 1, N, K) * K ** -0.5
+    if kind == "bf16":
+        x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+        W, X = (w.bfloat16(), None), (x, None)
+        w64 = W[0].double()
+    else:
+        x = torch.randint(0, 0x70, (M, K), dtype=torch.uint8, generator=g, device="cuda")
+        xs = torch.full((M, K // 32), 120, dtype=torch.uint8, device="cuda")
+        W, X = quantize(w), (x, xs)
+        w64 = value_of(*W)
+    o = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    run_matmul(pm, kind, W, X, M, None, offsets_of([M]), M, N, K, pm.BF16, o)
+    torch.cuda.synchronize()
+    at = torch.tensor([0, 1, 129, 262_143, 262_144, 300_001, 524_287, 524_288, 539_000, M - 1], device="cuda")
+    x64 = x[at].double() if kind == "bf16" else value_of(x[at], X[1][at])
+    p, d = products(x64, w64, [len(at)])
+    check_near(o[at], p, d, 2.0 ** -8)
+
+
+def test_grouped_matmul_experts_past_2_31_elements(pm):
+    K, N, E = 1024, 4096, 600
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    g = gen(13)
+    w = torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    c = [0] * E
+    c[0], c[511], c[512], c[599] = 2, 3, 4, 5
+    x = randn(g, 14, K).bfloat16()
+    o = empty(14, N, dtype=torch.float32)
+    run_matmul(pm, "bf16", (w, None), (x, None), 14, None, offsets_of(c), 14, N, K, pm.F32, o)
+    torch.cuda.synchronize()
+    live = [0, 511, 512, 599]
+    p, d = products(x.double(), w[live].double(), [c[e] for e in live])
+    check_near(o, p, d, U)
+
+
+def test_rows_past_2_31_elements(pm):
+    """Norm and combination on rows behind 2^31 elements."""
+    T, H = 600_000, 4096
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    r = torch.empty(T, H, device="cuda").normal_(generator=gen(14))
+    codes, scales = empty(T, H), empty(T, H // 32)
+    pm.residual_norm_q8(r, None, None, 0.0, T, H, codes, scales)
+    torch.cuda.synchronize()
+    at = torch.tensor([0, 524_287, 524_288, T - 1], device="cuda")
+    _, v, dv = norm_reference(r[at], None, None, 0.0)
+    check_q8(codes[at], scales[at], v, dv)
+    w = torch.full((T, 1), 0.5, device="cuda")
+    row_of = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")
+    y = torch.empty(T, H, device="cuda")
+    pm.combine_rows(r, False, row_of, w, T, 1, H, y)
+    torch.cuda.synchronize()
+    assert torch.equal(y[at], 0.5 * r[T - 1 - at])
