@@ -10,6 +10,9 @@
 // An SM takes in about 64 bytes per cycle: 48 KB take longer than the stage's MMAs (768 against 512 cycles at least),
 // which is what bounds long prompts. (Pairs of SMs sharing 256 x 256 tiles, 32 KB per SM and stage, gained 6 to 8 %
 // where experts have multiples of 256 rows and nothing on average over ragged ones.)
+// Measured: 16 experts of 1024 rows, 2048 x 4096: bf16 217 us (1268 TFLOP/s), q8 128 us (2140), with gathered rows 232
+// and 142 us; 300 experts of 40 rows, 4096 x 1024: 404 and 214 us (6.2 and 6.0 TB/s of weights); one token of ten
+// experts, q8 gate, up and SwiGLU, 2 x 1024 x 4096: 23 us, of which the weights stream for 13 (6.6 TB/s).
 // A persistent CTA per SM takes tiles at a stride of all of them: every role finds a tile's expert in a prefix
 // table of row tiles that the CTA makes from `offsets` when it starts. Roles, one warp each unless said otherwise:
 //   - producer: tiled TMA loads of 128 bytes of k per row into a ring of stages: the matrix rows and rows of x that
