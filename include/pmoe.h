@@ -359,6 +359,8 @@ PMOE_API pmoe_status pmoe_layer_error(const void *ws, int *code, int *detail, pm
  * started, records error 3 (see pmoe_layer_error) and finishes. Waits for the
  * kernel's own copies to land before it exits have a separate bound, 200 ms
  * past that one.
+ * In the grouped products the limit counts from the start of each wait (see
+ * pmoe_grouped_error).
  * 0 restores the default of 200 ms. Host only; the kernels stay correct with
  * any limit that is not reached.
  */
@@ -672,7 +674,8 @@ PMOE_API pmoe_status pmoe_grouped_matmul(const pmoe_dense *W, const pmoe_rows *X
  * pmoe_grouped_swiglu: the gate and up products of every expert and their
  * SwiGLU: with N = 2*I, rows 0..I-1 of W_e the gate and I..2I-1 the up matrix,
  *   h_r = silu(g) * u,  g = Wgate_e x_r, u = Wup_e x_r  (silu(g) = g / (1 + exp(-g))),
- * g, u and h in float, h rounded once. Rows and offsets as
+ * g, u and h in float (the exponential to 2 + |g| units in the last place),
+ * h rounded once. Rows and offsets as
  * pmoe_grouped_matmul.
  *   out_type PMOE_TYPE_BF16: h bf16 [rows][I], I % 8 == 0. PMOE_TYPE_Q8: h
  *   e4m3 codes [rows][I] and h_scales [rows][I/32], I % 32 == 0.
