@@ -278,7 +278,7 @@ pmoe_status pmoe_group_pairs(const int32_t *ids, int T, int k, int E, int32_t *o
     const cudaStream_t st = (cudaStream_t)stream;
     if (smem > 48 * 1024)
         PMOE_CUDA(cudaFuncSetAttribute(group_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem));
+                                       kGroupWarps * kMaxGroupExperts * (int)sizeof(int32_t)));
     int32_t *hist = blocks > 1 ? static_cast<int32_t *>(ws) : nullptr;
     if (hist)
         PMOE_TRY(launch_early(group_histogram_kernel, dim3(blocks), kGroupThreads, E * sizeof(int32_t), st, ids, (int)P,

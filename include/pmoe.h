@@ -585,8 +585,8 @@ PMOE_API pmoe_status pmoe_residual_norm(float *r, const float *y, int T, int H, 
  *
  * Device pointers are used on the current device: a call whose pointers are
  * not memory of that device returns PMOE_ERR_INVALID_ARG. Outputs must not
- * overlap inputs unless a call says so. Every call may be captured into a
- * graph, and calls on different streams do not disturb each other (each
+ * overlap inputs unless a call says so. Every call but pmoe_grouped_error
+ * (which waits) may be captured into a graph, and calls on different streams do not disturb each other (each
  * with its own outputs and workspace). Results do not depend on timing.
  *
  * "q8" rows: e4m3 codes (1 sign, 4 exponent, 3 mantissa bits; largest value

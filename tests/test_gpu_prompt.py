@@ -571,3 +571,54 @@ def test_rows_past_2_31_elements(pm):
     pm.combine_rows(r, False, row_of, w, T, 1, H, y)
     torch.cuda.synchronize()
     assert torch.equal(y[at], 0.5 * r[T - 1 - at])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+def test_grouped_rows_of_an_empty_x_are_zeros(pm, kind):
+    """No input rows at all: every index names a row outside."""
+    K, N = 256, 64
+    W, X, *_ = case(kind, [5, 40], K, N, 3, seed=15)
+    index = torch.tensor([0, 1, -1, 7, 2 ** 31 - 1] * 9, dtype=torch.int32, device="cuda")
+    o = torch.full((45, N), 7.0, device="cuda")
+    run_matmul(pm, kind, W, (None, None), 0, index, offsets_of([5, 40]), 45, N, K, pm.F32, o)
+    torch.cuda.synchronize()
+    assert not o.any()
+
+
+def test_calls_from_several_host_threads(pm):
+    """Different sizes at once from threads with streams of their own: the results of each call alone."""
+    import threading
+    jobs = []
+    for i, E in enumerate((8, 700, 2048, 33)):
+        ids = torch.randint(-1, E + 1, (900, 7), dtype=torch.int32, generator=gen(20 + i), device="cuda")
+        W, X, n, index, _, _ = case("q8", [30 + i, 0, 200 * i, 5], 256, 128, 60, seed=20 + i)
+        jobs.append((E, ids, W, X, n, index, [30 + i, 0, 200 * i, 5]))
+
+    def run(job, st):
+        E, ids, W, X, n, index, c = job
+        P, M = ids.numel(), sum(c)
+        o, r, t = (torch.zeros(k, dtype=torch.int32, device="cuda") for k in (E + 1, P, P))
+        ws = empty(pm.group_workspace_bytes(900, 7, E) + 16)
+        off = offsets_of(c)
+        h = torch.zeros(M, 128, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(20):
+            pm.group_pairs(ids, 900, 7, E, o, r, t, ws, ws.numel(), st)
+            run_matmul(pm, "q8", W, X, n, index, off, M, 128, 256, pm.F32, h, stream=st)
+        st.synchronize()
+        return o, r, t, h
+
+    want = [run(j, torch.cuda.current_stream()) for j in jobs]
+    got = [None] * len(jobs)
+
+    def work(i):
+        got[i] = run(jobs[i], torch.cuda.Stream())
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
