@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         pipe::mbar_init(&bars->done, 1);
         bars->abort = 0;
         pipe::fence_barrier_init();
-        tma::prefetch_map(&xmap);
+        if (!g.index)
+            tma::prefetch_map(&xmap);
         tma::prefetch_map(&wmap);
     }
     if (warp == 1) {
@@ -827,13 +828,15 @@ pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offs
         return PMOE_ERR_UNSUPPORTED;
     const int elem = is_q8 ? 1 : 2;
     const uint64_t K = (uint64_t)W->K;
-    Maps m;
+    Maps m{}; // no maps of x where it is gathered
     // no input rows at all: every index is outside, the map's one row is never read
     const void *x = X->n ? X->x : W->w;
     const uint64_t xd[2] = {K, (uint64_t)(X->n ? X->n : 1)}, xstride[1] = {K * elem};
     const uint32_t xbox[2] = {(uint32_t)(kRowBytes / elem), 32}, xwbox[2] = {(uint32_t)(kRowBytes / elem), 128};
-    PMOE_TRY(tma::make_map(&m.x, elem, 2, x, xd, xstride, xbox));
-    PMOE_TRY(tma::make_map(&m.xwide, elem, 2, x, xd, xstride, xwbox));
+    if (!X->index) {
+        PMOE_TRY(tma::make_map(&m.x, elem, 2, x, xd, xstride, xbox));
+        PMOE_TRY(tma::make_map(&m.xwide, elem, 2, x, xd, xstride, xwbox));
+    }
     // [E][gate, up][I][K] in boxes of 32 gate rows and the up rows of the same columns, or [E][1][N][K]
     const uint64_t halves = swiglu ? 2 : 1;
     const uint64_t wd[4] = {K, (uint64_t)width, halves, (uint64_t)W->E};

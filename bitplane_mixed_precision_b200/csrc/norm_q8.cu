@@ -20,7 +20,8 @@ __device__ __forceinline__ uint2 bf16x4(float4 v)
 
 // One block per token, V float4 of the row per thread, held in registers between the sum of squares and
 // the output: r and y are read once and r written once. 8 neighbouring lanes hold one 32-column block. Bound by memory:
-// 4096 x 4096 takes 39 us, 5.6 TB/s of the 13 bytes an element that have to move.
+// 4096 x 4096 takes 38 us, 5.8 TB/s of the 13 bytes an element that have to move (with r and y passed through the L2
+// as streams, which leaves its room to the codes that the next call reads: 37.9 us against 38.8).
 template <int V>
 __global__ void __launch_bounds__(kMaxNormThreads)
     residual_norm_q8_kernel(float *__restrict__ r, const float *__restrict__ y, const float *__restrict__ gain,
@@ -39,9 +40,9 @@ __global__ void __launch_bounds__(kMaxNormThreads)
         const int i = tid + j * blockDim.x;
         v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (i < n4) {
-            v[j] = *reinterpret_cast<const float4 *>(r + row + 4 * i);
+            v[j] = __ldcs(reinterpret_cast<const float4 *>(r + row + 4 * i));
             if (y != nullptr) {
-                const float4 d = __ldg(reinterpret_cast<const float4 *>(y + row + 4 * i));
+                const float4 d = __ldcs(reinterpret_cast<const float4 *>(y + row + 4 * i));
                 v[j].x += d.x;
                 v[j].y += d.y;
                 v[j].z += d.z;
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kMaxNormThreads)
     for (int j = 0; j < V; ++j) {
         const int i = tid + j * blockDim.x;
         if (y != nullptr && i < n4)
-            *reinterpret_cast<float4 *>(r + row + 4 * i) = v[j];
+            __stcs(reinterpret_cast<float4 *>(r + row + 4 * i), v[j]);
         ss = fmaf(v[j].x, v[j].x, ss);
         ss = fmaf(v[j].y, v[j].y, ss);
         ss = fmaf(v[j].z, v[j].z, ss);
