@@ -109,6 +109,17 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
 
+// One lane of a whole warp, the same every time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r));
+    return r != 0;
+}
+
 // A wait that gives up after limit_ns, or as soon as another role has given up.
 struct Waiter {
     Bars *b;
@@ -412,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ---- producer
+        const bool leader = elect_one();
         Ring<S::kStages> ring;
         for (int t = t0; t < tiles; t += step) {
             const Tile T = tile(t);
@@ -424,22 +436,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     goto produced;
                 uint8_t *a = smem + s * (S::kA + S::kB), *b = a + S::kA;
                 const int x = i * (kRowBytes / kElem);
-                if (lane == 0)
+                if (leader) {
                     pipe::mbar_arrive_expect_tx(&bars->full[s], bytes);
+#pragma unroll
+                    for (int j = 0; j < kBoxes; ++j)
+                        tma::load_4d(b + j * kBoxRows * kRowBytes, &wmap, x, T.col0 + j * kBoxCols, 0, T.e,
+                                     &bars->full[s]);
+                    for (int j = 0; j < loads; ++j)
+                        tma::load_2d(a + j * 32 * kRowBytes, one ? &xwide : &xmap, x, T.row0 + 32 * j, &bars->full[s]);
+                }
                 __syncwarp();
-                if (lane < kBoxes)
-                    tma::load_4d(b + lane * kBoxRows * kRowBytes, &wmap, x, T.col0 + lane * kBoxCols, 0, T.e,
-                                 &bars->full[s]);
-                else if (lane < kBoxes + loads)
-                    tma::load_2d(a + (lane - kBoxes) * 32 * kRowBytes, one ? &xwide : &xmap, x,
-                                 T.row0 + 32 * (lane - kBoxes), &bars->full[s]);
             }
         }
     produced:
         __syncwarp();
     } else if (warp == 1) {
-        // ---- MMA
-        if (lane == 0) {
+        // ---- MMA: the warp goes through the stages together, one lane issues
+        {
+            const bool leader = elect_one();
             Ring<S::kStages> ring;
             const uint64_t a0 = umma::smem_desc_sw128(smem), b0 = umma::smem_desc_sw128(smem + S::kA);
             bool ok = true;
@@ -448,41 +462,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the accumulator this tile takes: free since the epilogue's read of the last tile's shared
                 // columns (q8, 256 columns), or of all of the tile before that
                 const int free = S::kOverlap ? i - 1 : i - 2;
-                ok = free < 0 || wait(&bars->acc_free[free & 1], (free >> 1) & 1, 2);
+                ok = free < 0 || warp_wait(wait, &bars->acc_free[free & 1], (free >> 1) & 1, 2);
                 umma::fence_after_sync();
                 const uint32_t d = tmem + (i & 1) * S::kSecond;
                 for (int k = 0; ok && k < g.iters; ++k, ring.next()) {
                     const int s = ring.s;
-                    ok = wait(&bars->full[s], ring.phase, 3);
+                    ok = warp_wait(wait, &bars->full[s], ring.phase, 3);
                     if (!ok)
                         break;
                     umma::fence_after_sync();
                     const uint64_t ad = a0 + s * ((S::kA + S::kB) >> 4), bd = b0 + s * ((S::kA + S::kB) >> 4);
-                    if (Q8IN) {
-                        // a set of scale columns per stage: what read it last has finished, or the stage would not
-                        // be there
-                        const uint32_t sa = tmem + S::kScaleCols + 4 * s;
-                        const uint32_t sb = tmem + S::kScaleCols + 4 * S::kSets + 4 * S::kAtoms * s;
-                        const uint8_t *sc = smem + S::kScalesAt + s * S::kScales;
-                        umma::copy_scales(sa, sc);
-                        for (int j = 0; j < S::kAtoms; ++j)
-                            umma::copy_scales(sb + 4 * j, sc + 512 * (j + 1));
+                    if (leader) {
+                        if (Q8IN) {
+                            // a set of scale columns per stage: what read it last has finished, or the stage would
+                            // not be there
+                            const uint32_t sa = tmem + S::kScaleCols + 4 * s;
+                            const uint32_t sb = tmem + S::kScaleCols + 4 * S::kSets + 4 * S::kAtoms * s;
+                            const uint8_t *sc = smem + S::kScalesAt + s * S::kScales;
+                            umma::copy_scales(sa, sc);
+                            for (int j = 0; j < S::kAtoms; ++j)
+                                umma::copy_scales(sb + 4 * j, sc + 512 * (j + 1));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            umma::mma_mxf8(d, ad + 2 * j, bd + 2 * j, umma::idesc_mxf8(kLanes, NT, j), sa, sb,
-                                           (k | j) != 0);
-                    } else {
+                            for (int j = 0; j < 4; ++j)
+                                umma::mma_mxf8(d, ad + 2 * j, bd + 2 * j, umma::idesc_mxf8(kLanes, NT, j), sa, sb,
+                                               (k | j) != 0);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            umma::mma_f16(d, ad + 2 * j, bd + 2 * j, umma::idesc_bf16(kLanes, NT), (k | j) != 0);
+                            for (int j = 0; j < 4; ++j)
+                                umma::mma_f16(d, ad + 2 * j, bd + 2 * j, umma::idesc_bf16(kLanes, NT), (k | j) != 0);
+                        }
+                        umma::commit(&bars->empty[s]);
+                        if (k == g.iters - 1)
+                            umma::commit(&bars->acc_full[i & 1]);
                     }
-                    umma::commit(&bars->empty[s]);
+                    __syncwarp();
                 }
-                if (ok)
-                    umma::commit(&bars->acc_full[i & 1]);
             }
-            umma::commit(&bars->done);
-            drain(&bars->done, 0);
+            if (leader) {
+                umma::commit(&bars->done);
+                drain(&bars->done, 0);
+            }
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -516,13 +535,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (g.index) {
             Ring<S::kStages> ring;
             int left = t0 < tiles ? (tiles - t0 + step - 1) / step * g.iters : 0;
-            if (lane == 0)
-                for (; left > 0; --left, ring.next()) {
-                    if (!wait(&bars->gathered[ring.s], ring.phase, 11))
-                        break;
+            const bool leader = elect_one();
+            for (; left > 0; --left, ring.next()) {
+                if (!warp_wait(wait, &bars->gathered[ring.s], ring.phase, 11))
+                    break;
+                if (leader) {
                     umma::fence_smem_async();
                     pipe::mbar_arrive(&bars->full[ring.s]);
                 }
+                __syncwarp();
+            }
         }
         __syncwarp();
     } else if (warp >= 8) {
