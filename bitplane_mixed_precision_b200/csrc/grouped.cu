@@ -120,6 +120,19 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
+// mbar_try_wait that comes back after half a microsecond or so (without a hint it may take several).
+__device__ __forceinline__ bool mbar_try_wait_briefly(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(pipe::smem_u32(bar)), "r"(parity), "r"(500u)
+                 : "memory");
+    return ok != 0;
+}
+
 // A wait that gives up after limit_ns, or as soon as another role has given up.
 struct Waiter {
     Bars *b;
@@ -128,21 +141,18 @@ struct Waiter {
     {
         if (pipe::mbar_try_wait(bar, parity))
             return true;
-        const uint64_t deadline = pipe::globaltimer() + limit_ns;
-        for (int it = 1;; ++it) {
-            if (pipe::mbar_try_wait(bar, parity))
-                return true;
-            if ((it & 3) == 0) {
-                if (*reinterpret_cast<volatile int *>(&b->abort))
-                    return false;
-                if (pipe::globaltimer() > deadline) {
-                    *reinterpret_cast<volatile int *>(&b->abort) = 1;
-                    if (atomicCAS(&g_grouped_error[0], 0, 3) == 0)
-                        g_grouped_error[1] = where;
-                    return false;
-                }
+        const uint64_t start = pipe::globaltimer();
+        while (!mbar_try_wait_briefly(bar, parity)) {
+            if (*reinterpret_cast<volatile int *>(&b->abort))
+                return false;
+            if (pipe::globaltimer() - start >= limit_ns) {
+                *reinterpret_cast<volatile int *>(&b->abort) = 1;
+                if (atomicCAS(&g_grouped_error[0], 0, 3) == 0)
+                    g_grouped_error[1] = where;
+                return false;
             }
         }
+        return true;
     }
 };
 
@@ -557,28 +567,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = t0; t < tiles; t += step) {
                 const Tile T = tile(t);
                 const uint8_t *src[ROWS / 16];
+                uint32_t live = 0; // rows inside x
 #pragma unroll
                 for (int j = 0; j < ROWS / 16; ++j) {
                     const int r = r0 + 16 * j;
-                    src[j] = nullptr;
+                    src[j] = g.x + 16 * chunk;
                     if (r < T.rows) {
                         const int i = __ldg(g.index + T.row0 + r);
-                        if ((uint32_t)i < (uint32_t)g.n)
-                            src[j] = g.x + i * pitch + 16 * chunk;
+                        if ((uint32_t)i < (uint32_t)g.n) {
+                            src[j] += i * pitch;
+                            live |= 1u << j;
+                        }
                     }
                 }
                 for (int i = 0; i < g.iters; ++i, ring.next()) {
                     if (!ring.free(wait, bars, 9))
                         goto gathered;
                     const uint32_t dst = pipe::smem_u32(smem + ring.s * (S::kA + S::kB)) + at;
-                    const bool in = i * kRowBytes + 16 * chunk < pitch;
+                    const uint32_t off = (uint32_t)i * kRowBytes;
+                    const bool in = off + 16 * chunk < pitch;
 #pragma unroll
                     for (int j = 0; j < ROWS / 16; ++j)
                         // rows outside x, and k behind K, are filled with zeros; so is, the first time round, what the
                         // last tile left behind this one's rows
                         if (r0 + 16 * j < T.rows || i < S::kStages)
-                            copy16(dst + j * 16 * kRowBytes, src[j] && in ? src[j] + i * kRowBytes : g.x,
-                                   src[j] && in ? 16 : 0);
+                            copy16(dst + j * 16 * kRowBytes, src[j] + off, in && (live >> j & 1) ? 16 : 0);
                     copies_arrive(&bars->gathered[ring.s]);
                 }
             }
