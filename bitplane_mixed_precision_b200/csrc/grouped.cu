@@ -10,9 +10,9 @@
 // An SM takes in about 64 bytes per cycle: 48 KB take longer than the stage's MMAs (768 against 512 cycles at least),
 // which is what bounds long prompts. (Pairs of SMs sharing 256 x 256 tiles, 32 KB per SM and stage, gained 6 to 8 %
 // where experts have multiples of 256 rows and nothing on average over ragged ones.)
-// Measured: 16 experts of 1024 rows, 2048 x 4096: bf16 217 us (1268 TFLOP/s), q8 128 us (2140), with gathered rows 232
-// and 142 us; 300 experts of 40 rows, 4096 x 1024: 404 and 214 us (6.2 and 6.0 TB/s of weights); one token of ten
-// experts, q8 gate, up and SwiGLU, 2 x 1024 x 4096: 23 us, of which the weights stream for 13 (6.6 TB/s).
+// Measured: 16 experts of 1024 rows, 2048 x 4096: bf16 217 us (1265 TFLOP/s), q8 122 us (2244), with gathered rows 224
+// and 131 us; 300 experts of 40 rows, 4096 x 1024: 404 and 215 us (6.2 and 6.0 TB/s of weights); one token of ten
+// experts, q8 gate, up and SwiGLU, 2 x 1024 x 4096: 21 us, of which the weights stream for 13 (6.6 TB/s).
 // A persistent CTA per SM takes tiles at a stride of all of them: every role finds a tile's expert in a prefix
 // table of row tiles that the CTA makes from `offsets` when it starts. Roles, one warp each unless said otherwise:
 //   - producer: tiled TMA loads of 128 bytes of k per row into a ring of stages: the matrix rows and rows of x that
@@ -24,8 +24,10 @@
 //     them over as they land (2 to 4 % faster than the four waiting for copies of their own two stages back);
 //   - q8: two warps bring the scale bytes (one word per row and stage) into the order the tensor cores take, loaded
 //     several stages ahead;
-//   - MMA: one thread, which waits for one barrier per stage (a second wait and a fence of its own per stage cost the
-//     q8 products 10 to 20 %: everybody else fences and arrives on that one barrier); four K slices per stage,
+//   - MMA: one elected lane issues, its warp waits for one barrier per stage with it (a second wait and a fence of its
+//     own per stage cost the q8 products 10 to 20 %: everybody else fences and arrives on that one barrier; and behind
+//     a branch on the lane's number instead of an election, in a warp that does not stay together, the same
+//     instructions took 10 % longer); four K slices per stage,
 //     accumulators in tensor memory: two of NT columns. q8 needs tensor memory for scales too, so its two of 256 share
 //     64 columns: the next tile starts once the epilogue has read those, which it does first;
 //   - epilogue, four warps (one per quarter of the tensor-memory lanes = 32 rows): SwiGLU and the rounding on
