@@ -12,6 +12,8 @@ namespace tma {
 // Map of a row-major tensor of `rank` dimensions (innermost first; strides in bytes of dimensions 1..) whose
 // box's rows are 128 bytes, stored with the 128-byte swizzle (16-byte chunk ^= row % 8). Elements outside the
 // tensor read as zeros.
+// Misses fetch 256 bytes into the L2, half of them the next box's along a row: the 2048-token q8 down products over
+// 512 experts took 357 us against 393 with 128 bytes, or none, of promotion.
 inline pmoe_status make_map(CUtensorMap *map, int elem_bytes, int rank, const void *base, const uint64_t *dims,
                             const uint64_t *strides, const uint32_t *box)
 {
