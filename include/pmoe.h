@@ -678,9 +678,9 @@ PMOE_API pmoe_status pmoe_grouped_matmul(const pmoe_dense *W, const pmoe_rows *X
  * pmoe_grouped_swiglu: the gate and up products of every expert and their
  * SwiGLU: with N = 2*I, rows 0..I-1 of W_e the gate and I..2I-1 the up matrix,
  *   h_r = silu(g) * u,  g = Wgate_e x_r, u = Wup_e x_r  (silu(g) = g / (1 + exp(-g))),
- * g, u and h in float (the exponential to 2 + |g| units in the last place),
- * h rounded once. Rows and offsets as
- * pmoe_grouped_matmul.
+ * g, u and h in float, h rounded once. silu(g) * u is within 17 + |g| / 20
+ * half units in the last place of a float (and within a step of the subnormal
+ * floats in exp(-|g|)). Rows and offsets as pmoe_grouped_matmul.
  *   out_type PMOE_TYPE_BF16: h bf16 [rows][I], I % 8 == 0. PMOE_TYPE_Q8: h
  *   e4m3 codes [rows][I] and h_scales [rows][I/32], I % 32 == 0.
  */

@@ -1,0 +1,66 @@
+"""Ends of the prompt-side operators' ranges on the GPU: arguments, magnitudes and orders of calls at which a form
+that is right elsewhere can be wrong."""
+import pytest
+import torch
+
+from prompt_common import U, check_near, check_q8, offsets_of, quantize
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pm():
+    import bitplane_mixed_precision_b200 as pm
+    return pm
+
+
+def empty(*shape, dtype=torch.uint8):
+    return torch.empty(*shape, dtype=dtype, device="cuda")
+
+
+# ---------------------------------------------------------------- SwiGLU
+
+@pytest.mark.parametrize("rows", [3, 200])
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("out", ["bf16", "q8"])
+def test_swiglu_of_large_gates(pm, rows, kind, out):
+    """One product a sum, all of them exact, so that SwiGLU's own error is what is seen: 17 + |g| / 20 roundings, and,
+    where exp(-|g|) is subnormal, a step of the subnormals in it. Up values near 2^100 bring what is left into range."""
+    K, I = 128, 64
+    gates = [-104.0, -96.0, -88.0, -80.0, -30.0, -0.5, 0.0, 0.5, 30.0, 88.0, 104.0]
+    g = torch.tensor((gates * 6)[:I], device="cuda")
+    u = torch.where(g < -60, 2.0 ** 100, 1.5)
+    x, w = torch.zeros(rows, K, device="cuda"), torch.zeros(1, 2 * I, K, device="cuda")
+    x[:, 0], w[0, :I, 0], w[0, I:, 0] = 1.0, g, u
+    t = pm.Q8 if kind == "q8" else pm.BF16
+    (xc, xs), (wc, ws) = (quantize(x), quantize(w)) if kind == "q8" else ((x.bfloat16(), None), (w.bfloat16(), None))
+    h = empty(rows, I, dtype=torch.uint8 if out == "q8" else torch.bfloat16)
+    hs = empty(rows, I // 32) if out == "q8" else None
+    pm.grouped_swiglu(pm.make_dense(t, wc, ws, 1, 2 * I, K), pm.make_rows(t, xc, xs, rows), offsets_of([rows]), rows,
+                      pm.Q8 if out == "q8" else pm.BF16, h, hs)
+    torch.cuda.synchronize()
+    g, u = g.double().expand(rows, I), u.double().expand(rows, I)
+    v = g * torch.sigmoid(g) * u
+    dv = (17 + g.abs() / 20) * U * v.abs() + (g.abs() + 1) * 2.0 ** -149 * u
+    if out == "q8":
+        check_q8(h, hs, v, dv)
+    else:
+        check_near(h, v, dv, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_swiglu_of_gates_that_are_not_finite(pm, rows):
+    """The formula's values: inf * u for a gate of +inf, and NaN for -inf (-inf * 0) and NaN; zeros far below zero."""
+    K, I = 64, 64
+    gates = [float("inf"), float("-inf"), float("nan"), 3e38, -3e38, -1000.0, 1.0, 0.0]
+    g = torch.tensor(gates * (I // 8), device="cuda").bfloat16()
+    x, w = (torch.zeros(*s, dtype=torch.bfloat16, device="cuda") for s in ((rows, K), (1, 2 * I, K)))
+    x[:, 0], w[0, :I, 0], w[0, I:, 0] = 1.0, g, 0.5
+    h = empty(rows, I, dtype=torch.bfloat16)
+    pm.grouped_swiglu(pm.make_dense(pm.BF16, w, None, 1, 2 * I, K), pm.make_rows(pm.BF16, x, None, rows),
+                      offsets_of([rows]), rows, pm.BF16, h, None)
+    torch.cuda.synchronize()
+    h = h.view(rows, I // 8, 8).float()
+    assert bool((h[..., 0] == float("inf")).all()) and bool(h[..., 1:3].isnan().all())
+    assert bool((h[..., 3] == 0.5 * g[3].float()).all()) and not h[..., [4, 5, 7]].any()
+    assert bool(((h[..., 6] - 0.5 * torch.sigmoid(torch.tensor(1.0))).abs() <= 2.0 ** -9 * 0.5).all())
