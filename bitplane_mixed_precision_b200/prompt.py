@@ -72,7 +72,8 @@ class DenseExperts:
 
 class PromptLayer:
     """Buffers for up to max_tokens tokens through one layer's experts, k of them each. Calls that overlap
-    on the GPU need a PromptLayer each (they may share the experts)."""
+    on the GPU need a PromptLayer each (they may share the experts). Calls run on the stream given, or on
+    torch's current stream of the layer's device; keep the layer until what they enqueued has finished."""
 
     def __init__(self, experts: DenseExperts, k: int, max_tokens: int):
         self.experts, self.k, self.max_tokens = experts, k, max_tokens
@@ -96,10 +97,13 @@ class PromptLayer:
         if not 0 <= T <= self.max_tokens:
             raise ValueError(f"{T} tokens in a layer of {self.max_tokens}")
 
+    def _stream(self, stream):
+        return stream if stream is not None else torch.cuda.current_stream(self.y.device)
+
     def norm(self, r, y, T: int, gain=None, eps: float = 0.0, stream=None) -> None:
         """The layer's input from the residual stream: r += y (y may be None), x = r / rms(r) * gain."""
         self._tokens(T)
-        x = self.experts
+        x, stream = self.experts, self._stream(stream)
         if x.kind == Q8:
             residual_norm_q8(r, y, gain, eps, T, x.H, self.x, self.x_scales, None, stream)
         else:
@@ -108,13 +112,13 @@ class PromptLayer:
     def route(self, logits, T: int, stream=None) -> None:
         """Experts and weights of the first T tokens from their router logits [T, E]."""
         self._tokens(T)
-        route(logits, T, self.experts.E, self.k, self.ids, self.w, stream)
+        route(logits, T, self.experts.E, self.k, self.ids, self.w, self._stream(stream))
 
     def forward(self, T: int, stream=None) -> torch.Tensor:
         """The layer's output [T, H] for the first T rows of x, ids and w (an id outside 0..E-1 marks a
         slot that no expert takes). The tensor is the layer's own buffer."""
         self._tokens(T)
-        x, k, P = self.experts, self.k, T * self.k
+        x, k, P, stream = self.experts, self.k, T * self.k, self._stream(stream)
         group_pairs(self.ids, T, k, x.E, self.offsets, self.row_of, self.token_of, self.ws, self.ws.numel(), stream)
         rows = make_rows(x.kind, self.x, self.x_scales, T, self.token_of)
         grouped_swiglu(x.up_dense, rows, self.offsets, P, x.kind, self.h, self.h_scales, stream)
