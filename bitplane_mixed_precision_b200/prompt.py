@@ -56,7 +56,8 @@ class DenseExperts:
         """A stored layer's experts at the given depth."""
         dev = R.pool.device
         st = stream if stream is not None else torch.cuda.current_stream(dev)
-        idx = torch.empty(R.H * R.I, dtype=torch.uint8, device=dev)
+        with torch.cuda.device(dev), torch.cuda.stream(st):  # torch takes its memory back in the order of this stream
+            idx = torch.empty(R.H * R.I, dtype=torch.uint8, device=dev)
         level = slice((1 << depth) - 2, (1 << (depth + 1)) - 2)
 
         def fill(e, m, w):

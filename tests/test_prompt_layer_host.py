@@ -44,3 +44,39 @@ def test_calls_run_on_the_current_stream_or_the_given_one(monkeypatch, calls, ki
     assert [n for n, _ in calls] == list(CALLS)
     assert all(a[-1] == ("the given stream" if given else "the current stream") for _, a in calls)
     assert all(d == L.y.device for d in asked)
+
+
+def test_decoding_a_stored_layer_allocates_on_its_own_stream(monkeypatch):
+    """torch gives memory freed on the host to later work of the stream that it was allocated on: a buffer of
+    another stream could be written again while the decoding still reads it."""
+    from bitplane_mixed_precision_b200 import prompt
+    from bitplane_mixed_precision_b200.store import ResidentLayer
+    now = ["the current stream"]
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, now[0] = now[0], stream
+        yield
+        now[0] = before
+
+    new, made = torch.empty, []
+
+    def empty(*a, **kw):
+        made.append(now[0])
+        return new(*a, **kw).zero_()
+
+    E, H, I, G = 2, 128, 128, 128
+    R = ResidentLayer.__new__(ResidentLayer)
+    R.E, R.H, R.I, R.G, R.mat_words = E, H, I, G, H * I // 32
+    R.slot_words, R.scale_len = 3 * R.mat_words, 2 * I * (H // G) + H * (I // G)
+    R.pool = torch.zeros(E * 8 * R.slot_words, dtype=torch.int32)
+    R.scales, R.codebooks = torch.ones(E * R.scale_len), torch.zeros(E * 3 * 510)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch, "empty", empty)
+    streams = []
+    monkeypatch.setattr(prompt, "extract_prefix", lambda *a: streams.append(a[-1]))
+    X = prompt.DenseExperts.from_layer(R, prompt.BF16, stream="the given stream")
+    assert X.up.shape == (E, 2 * I, H)
+    assert set(streams) == {"the given stream"} and len(streams) == 3 * E
+    assert len(made) >= 4 and set(made) == {"the given stream"}
