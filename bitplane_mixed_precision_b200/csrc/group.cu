@@ -276,7 +276,7 @@ pmoe_status pmoe_group_pairs(const int32_t *ids, int T, int k, int E, int32_t *o
     const int chunk = (int)(((P + blocks - 1) / blocks + 32 * kGroupWarps - 1) / (32 * kGroupWarps) * (32 * kGroupWarps));
     const size_t smem = (size_t)kGroupWarps * E * sizeof(int32_t);
     const cudaStream_t st = (cudaStream_t)stream;
-    if (smem > 48 * 1024)
+    if (smem + kGroupWarps * sizeof(int32_t) > 48 * 1024) // with the scan's static words
         PMOE_CUDA(cudaFuncSetAttribute(group_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kGroupWarps * kMaxGroupExperts * (int)sizeof(int32_t)));
     int32_t *hist = blocks > 1 ? static_cast<int32_t *>(ws) : nullptr;

@@ -1,5 +1,9 @@
 """Ends of the prompt-side operators' ranges on the GPU: arguments, magnitudes and orders of calls at which a form
 that is right elsewhere can be wrong."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -64,3 +68,29 @@ def test_swiglu_of_gates_that_are_not_finite(pm, rows):
     assert bool((h[..., 0] == float("inf")).all()) and bool(h[..., 1:3].isnan().all())
     assert bool((h[..., 3] == 0.5 * g[3].float()).all()) and not h[..., [4, 5, 7]].any()
     assert bool(((h[..., 6] - 0.5 * torch.sigmoid(torch.tensor(1.0))).abs() <= 2.0 ** -9 * 0.5).all())
+
+
+# ---------------------------------------------------------------- pairs by expert
+
+COUNTERS = """
+import sys
+import numpy as np
+import torch
+import bitplane_mixed_precision_b200 as pm
+E, T, k = int(sys.argv[1]), 300, 3
+ids = np.random.default_rng(E).integers(0, E, (T, k)).astype(np.int32)
+o, r, t = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (E + 1, T * k, T * k))
+pm.group_pairs(torch.from_numpy(ids).cuda(), T, k, E, o, r, t)
+order = np.argsort(ids.reshape(-1), kind="stable")
+assert np.array_equal(t.cpu().numpy(), order // k)
+assert np.array_equal(o.cpu().numpy()[1:], np.cumsum(np.bincount(ids.reshape(-1), minlength=E)))
+"""
+
+
+@pytest.mark.parametrize("E", [767, 768, 769])
+def test_group_pairs_where_its_counters_fill_48_kb(E):
+    """16 counters an expert are 48 KB at 768 experts, what a block has without asking for more. In a process of its
+    own: once a call has asked for more, the next ones have it."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", COUNTERS, str(E)], cwd=root, capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0, run.stderr
