@@ -43,7 +43,7 @@ class Dense(ctypes.Structure):
 
 class Rows(ctypes.Structure):
     """pmoe_rows: the input rows of a grouped product (device pointers)."""
-    _fields_ = [("type", i32), ("n", i32), ("x", P), ("scales", P), ("index", P)]
+    _fields_ = [("type", i32), ("n", i32), ("x", P), ("scales", P), ("index", P), ("error", P)]
 
 
 BF16, Q8, F32 = 0, 1, 2  # pmoe_type
@@ -385,10 +385,11 @@ def make_dense(type, w, scales, E, N, K) -> Dense:
     return Dense(type, E, N, K, _dense_ptr(w), _dense_ptr(scales))
 
 
-def make_rows(type, x, scales, n, index=None) -> Rows:
-    """n rows of x; index: int32, the x row of every sorted row (None: the sorted row itself). The caller
+def make_rows(type, x, scales, n, index=None, error=None) -> Rows:
+    """n rows of x; index: int32, the x row of every sorted row (None: the sorted row itself); error: int32 [2],
+    8-byte aligned, the calls' own record of a wait that ran out (None: the device's, grouped_error). The caller
     keeps the tensors alive."""
-    return Rows(type, n, _dense_ptr(x), _dense_ptr(scales), _dense_ptr(index))
+    return Rows(type, n, _dense_ptr(x), _dense_ptr(scales), _dense_ptr(index), _dense_ptr(error))
 
 
 def grouped_matmul(W: Dense, X: Rows, offsets, rows, out_type, out, stream=None) -> None:
@@ -405,7 +406,8 @@ def grouped_swiglu(W: Dense, X: Rows, offsets, rows, out_type, h, h_scales=None,
 
 
 def grouped_error(stream=None):
-    """(code, detail) of a wait that ran out in a grouped product, cleared by the call (synchronises)."""
+    """(code, detail) of a wait that ran out in a grouped product without a record of its own, on any stream of the
+    device; cleared by the call (synchronises)."""
     code, detail = i32(0), i32(0)
     _check("pmoe_grouped_error", _lib.pmoe_grouped_error(ctypes.byref(code), ctypes.byref(detail), _stream(stream)))
     return code.value, detail.value

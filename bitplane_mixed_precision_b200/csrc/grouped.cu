@@ -33,11 +33,12 @@
 //   - epilogue, four warps (one per quarter of the tensor-memory lanes = 32 rows): SwiGLU and the rounding on
 //     registers (a thread has 32 neighbouring columns of one row: a whole q8 block), then through shared memory so
 //     that rows are stored in pieces of 128 bytes.
-// Every wait is bounded; a wait that runs out is recorded (pmoe_grouped_error) and the CTA's roles finish in
-// turn, after their copies and MMAs in flight have landed.
+// Every wait is bounded; a wait that runs out is recorded (pmoe_rows.error, or the device's record) and the CTA's roles
+// finish in turn, after their copies and MMAs in flight have landed.
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "common.h"
 #include "layer.cuh"
@@ -58,8 +59,11 @@ constexpr int kStageRowBytes = 128;               // epilogue staging: bytes per
 constexpr uint64_t kDrainNs = 1000ull * 1000 * 1000;
 constexpr uint64_t kSettleNs = 5ull * 1000 * 1000; // hundreds of times what a load takes
 
-// the first wait that ran out in any grouped product since pmoe_grouped_error last read it: code 3 and which
-__device__ int g_grouped_error[2];
+// A record of the first wait that ran out, {code 3, which}, as one word that is written and taken in one step. This one
+// is for calls without a record of their own, since pmoe_grouped_error last took it.
+using Record = unsigned long long;
+__device__ Record g_grouped_error;
+__device__ Record g_taken; // pmoe_grouped_error's answer, one caller at a time
 
 struct Grouped {
     int E, N, K, n, rows, width, iters, ntiles; // width: output columns; iters: stages per tile
@@ -67,6 +71,7 @@ struct Grouped {
     const int32_t *index, *offsets;
     void *out;
     uint8_t *out_scales;
+    Record *error; // NULL: the device's
     uint64_t limit_ns;
 };
 
@@ -139,6 +144,7 @@ __device__ __forceinline__ bool mbar_try_wait_briefly(uint64_t *bar, uint32_t pa
 struct Waiter {
     Bars *b;
     uint64_t limit_ns;
+    Record *error;
     __device__ bool operator()(uint64_t *bar, uint32_t parity, int where) const
     {
         if (pipe::mbar_try_wait(bar, parity))
@@ -149,8 +155,7 @@ struct Waiter {
                 return false;
             if (pipe::globaltimer() - start >= limit_ns) {
                 *reinterpret_cast<volatile int *>(&b->abort) = 1;
-                if (atomicCAS(&g_grouped_error[0], 0, 3) == 0)
-                    g_grouped_error[1] = where;
+                atomicCAS(error ? error : &g_grouped_error, 0ull, 3ull | (Record)where << 32);
                 return false;
             }
         }
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     umma::fence_after_sync();
     const uint32_t tmem = bars->tmem;
     const int tiles = first[g.E] * g.ntiles, t0 = blockIdx.x, step = gridDim.x;
-    const Waiter wait{bars, g.limit_ns};
+    const Waiter wait{bars, g.limit_ns, g.error};
     Walk<ROWS> tile(g, first, kCols);
 
     if (warp == 0) {
@@ -800,6 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+__global__ void take_error_kernel() { g_taken = atomicExch(&g_grouped_error, 0ull); }
+
 struct Maps {
     CUtensorMap x, xwide, w;
 };
@@ -861,13 +868,14 @@ pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offs
     if (out_type == PMOE_TYPE_Q8 ? (width % 32 || (rows && !out_scales)) : out_scales != nullptr)
         return PMOE_ERR_INVALID_ARG;
     if (!aligned(W->w, 16) || !aligned(W->scales, 16) || !aligned(X->x, 16) || !aligned(X->scales, 16) ||
-        !aligned(X->index, 4) || !aligned(offsets, 4) || !aligned(out, 16) || !aligned(out_scales, 4))
+        !aligned(X->index, 4) || !aligned(X->error, 8) || !aligned(offsets, 4) || !aligned(out, 16) ||
+        !aligned(out_scales, 4))
         return PMOE_ERR_INVALID_ARG;
     if (W->E > kMaxDenseExperts)
         return PMOE_ERR_UNSUPPORTED;
     if (rows == 0)
         return PMOE_OK;
-    PMOE_TRY(on_current_device({W->w, W->scales, X->x, X->scales, X->index, offsets, out, out_scales}));
+    PMOE_TRY(on_current_device({W->w, W->scales, X->x, X->scales, X->index, X->error, offsets, out, out_scales}));
 
     // Rows of x per tile by the rows an expert has on average: at 16, tiles of 32 against 128 took 181 against 176 us
     // (q8, 256 experts of 4096 x 1024), 177 against 187 (q8 SwiGLU), 333 against 339 (bf16); at 32, 227 against 182 and
@@ -902,7 +910,7 @@ pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offs
     PMOE_TRY(tma::make_map(&m.w, elem, 4, W->w, wd, wstride, wbox));
     const Grouped g{W->E,      W->N,     W->K,      X->n,    rows, width,      (int)((K * elem + kRowBytes - 1) / kRowBytes),
                     ntiles, static_cast<const uint8_t *>(x), W->scales, X->scales, X->index, offsets, out, out_scales,
-                    wait_limit_ns()};
+                    reinterpret_cast<Record *>(X->error), wait_limit_ns()};
     const int64_t tiles = most * ntiles;
     const cudaStream_t st = (cudaStream_t)stream;
     return is_q8 ? launch_shape<true>(tile_rows, nt, swiglu, out_type, m, g, tiles, st)
@@ -932,15 +940,19 @@ pmoe_status pmoe_grouped_error(int *code, int *detail, pmoe_stream stream)
 {
     if (!code)
         return PMOE_ERR_INVALID_ARG;
-    int f[2];
+    static std::mutex one; // g_taken is the caller's from the exchange to the copy
+    const std::lock_guard<std::mutex> lock(one);
+    const cudaStream_t st = (cudaStream_t)stream;
+    Record r = 0;
     void *p = nullptr;
-    PMOE_CUDA(cudaGetSymbolAddress(&p, g_grouped_error));
-    PMOE_CUDA(cudaMemcpyAsync(f, p, sizeof(f), cudaMemcpyDeviceToHost, (cudaStream_t)stream));
-    PMOE_CUDA(cudaMemsetAsync(p, 0, sizeof(f), (cudaStream_t)stream));
-    PMOE_CUDA(cudaStreamSynchronize((cudaStream_t)stream));
-    *code = f[0];
+    PMOE_CUDA(cudaGetSymbolAddress(&p, g_taken));
+    take_error_kernel<<<1, 1, 0, st>>>();
+    PMOE_TRY(launch_status());
+    PMOE_CUDA(cudaMemcpyAsync(&r, p, sizeof(r), cudaMemcpyDeviceToHost, st));
+    PMOE_CUDA(cudaStreamSynchronize(st));
+    *code = (int)(uint32_t)r;
     if (detail)
-        *detail = f[1];
+        *detail = (int)(r >> 32);
     return PMOE_OK;
 }
 

@@ -93,6 +93,9 @@ class PromptLayer:
         self.h_scales = new(P, I // 32, dtype=torch.uint8) if q8 else None
         self.out = new(P, H, dtype=torch.bfloat16)
         self.y = new(T, H, dtype=torch.float32)
+        self.errors = torch.zeros(2, dtype=torch.int32, device=dev)
+        if dev.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()  # calls may come on any stream
 
     def _tokens(self, T: int) -> None:
         if not 0 <= T <= self.max_tokens:
@@ -117,13 +120,23 @@ class PromptLayer:
 
     def forward(self, T: int, stream=None) -> torch.Tensor:
         """The layer's output [T, H] for the first T rows of x, ids and w (an id outside 0..E-1 marks a
-        slot that no expert takes). The tensor is the layer's own buffer."""
+        slot that no expert takes). The tensor is the layer's own buffer. After a wait that ran out on the GPU
+        it is not complete: see error()."""
         self._tokens(T)
         x, k, P, stream = self.experts, self.k, T * self.k, self._stream(stream)
         group_pairs(self.ids, T, k, x.E, self.offsets, self.row_of, self.token_of, self.ws, self.ws.numel(), stream)
-        rows = make_rows(x.kind, self.x, self.x_scales, T, self.token_of)
+        rows = make_rows(x.kind, self.x, self.x_scales, T, self.token_of, self.errors)
         grouped_swiglu(x.up_dense, rows, self.offsets, P, x.kind, self.h, self.h_scales, stream)
-        rows = make_rows(x.kind, self.h, self.h_scales, P)
+        rows = make_rows(x.kind, self.h, self.h_scales, P, None, self.errors)
         grouped_matmul(x.down_dense, rows, self.offsets, P, BF16, self.out, stream)
         combine_rows(self.out, True, self.row_of, self.w, T, k, x.H, self.y, stream)
         return self.y[:T]
+
+    def error(self, stream=None):
+        """(code, detail) of the first wait that ran out in this layer's products (code 3; 0: none) since the last
+        such call, after what the stream holds (waits for it)."""
+        st = self._stream(stream)
+        with torch.cuda.stream(st if hasattr(st, "cuda_stream") else torch.cuda.ExternalStream(int(st), self.y.device)):
+            code, detail = self.errors.tolist()
+            self.errors.zero_()
+        return code, detail

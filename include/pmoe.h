@@ -654,6 +654,8 @@ typedef struct {
     const void *x;         /* [n][K] bf16 or e4m3 codes */
     const uint8_t *scales; /* q8: [n][K/32]; bf16: NULL */
     const int32_t *index;  /* sorted row r reads x row index[r]; NULL: row r itself */
+    int32_t *error;        /* device int32[2], 8-byte aligned: the calls' own record of a wait that ran out; NULL: the
+                              device's (pmoe_grouped_error) */
 } pmoe_rows;
 
 /*
@@ -688,10 +690,17 @@ PMOE_API pmoe_status pmoe_grouped_swiglu(const pmoe_dense *W, const pmoe_rows *X
                                          int out_type, void *h, uint8_t *h_scales, pmoe_stream stream);
 
 /*
- * pmoe_grouped_error: whether a bounded wait inside a grouped product ran out
- * (pmoe_set_wait_limit_ns; its output is then not complete) since the last
- * such call on the current device. Waits for the stream; *code is 0 or 3,
- * detail (may be NULL) names the wait; the record is cleared.
+ * A bounded wait inside a grouped product that runs out (pmoe_set_wait_limit_ns)
+ * leaves the output incomplete: rows may hold what was there before. The first
+ * one is recorded as {3, which wait}: in pmoe_rows.error, where calls that
+ * share it are the only ones that write it and the caller clears it ({0, 0})
+ * and reads it, in stream order; or else in one record of the device, shared
+ * by the calls of all streams.
+ *
+ * pmoe_grouped_error: takes the device's record (in one step: nothing that is
+ * recorded meanwhile is lost), whichever stream's call left it. Waits for the
+ * stream; *code is 0 or 3, detail (may be NULL) names the wait; the record is
+ * then clear, for every stream.
  */
 PMOE_API pmoe_status pmoe_grouped_error(int *code, int *detail, pmoe_stream stream);
 

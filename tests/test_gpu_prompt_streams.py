@@ -73,3 +73,99 @@ def test_a_layer_follows_the_current_stream(pm, kind):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, w)
+
+
+# ---------------------------------------------------------------- records of a wait that ran out
+
+@pytest.fixture
+def short_waits(pm):
+    """A wait limit of 1 ns while the context is open: the accumulators of a 8192-deep product take longer."""
+    class Limit:
+        def __enter__(self):
+            pm.set_wait_limit_ns(1)
+
+        def __exit__(self, *_):
+            torch.cuda.synchronize()
+            pm.set_wait_limit_ns(0)
+
+    yield Limit()
+    pm.set_wait_limit_ns(0)
+
+
+class Product:
+    """One expert's product, 700 x 8192 x 512."""
+    def __init__(self, pm, seed):
+        g = gen(seed)
+        M, K, N = 700, 8192, 512
+        self.x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+        self.w = torch.randn(1, N, K, generator=g, device="cuda").bfloat16()
+        self.offsets = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+        self.out = torch.empty(M, N, device="cuda")
+        self.error = torch.zeros(2, dtype=torch.int32, device="cuda")
+        self.dense, self.M = pm.make_dense(pm.BF16, self.w, None, 1, N, K), M
+
+    def __call__(self, pm, own, stream=None):
+        rows = pm.make_rows(pm.BF16, self.x, None, self.M, None, self.error if own else None)
+        pm.grouped_matmul(self.dense, rows, self.offsets, self.M, pm.F32, self.out, stream)
+
+
+def test_calls_with_a_record_of_their_own(pm, short_waits):
+    """A call's failure shows in its own record alone, and another caller's check does not clear it."""
+    a, b = Product(pm, 1), Product(pm, 2)
+    a(pm, True)
+    b(pm, True)
+    torch.cuda.synchronize()
+    want = a.out.clone()
+    assert pm.grouped_error() == (0, 0) and a.error.tolist() == [0, 0]
+    side = torch.cuda.Stream()
+    with short_waits:
+        a(pm, True, side)
+    b(pm, True)
+    assert pm.grouped_error() == (0, 0)
+    assert a.error.tolist()[0] == 3 and b.error.tolist() == [0, 0]
+    first = a.error.tolist()
+    with short_waits:
+        a(pm, True)
+    assert a.error.tolist() == first  # the first one stays until it is cleared
+    a.error.zero_()
+    a(pm, True)
+    torch.cuda.synchronize()
+    assert a.error.tolist() == [0, 0] and torch.equal(a.out, want)
+
+
+def test_the_device_s_record_is_taken_once_from_any_stream(pm, short_waits):
+    a = Product(pm, 3)
+    a(pm, False)
+    assert pm.grouped_error() == (0, 0)
+    side = torch.cuda.Stream()
+    with short_waits:
+        a(pm, False)
+    code, detail = pm.grouped_error(side)
+    assert code == 3 and detail > 0
+    assert pm.grouped_error() == (0, 0) and a.error.tolist() == [0, 0]
+
+
+def test_a_record_that_is_not_device_memory_is_refused(pm):
+    a = Product(pm, 4)
+    a.error = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(pm.PmoeError) as ei:
+        a(pm, True)
+    assert ei.value.code == 1
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_a_layer_reports_a_wait_that_ran_out(pm, short_waits, kind):
+    E, H, I, k, T = 4, 8192, 512, 2, 600
+    X = experts(kind, E, H, I, 5)
+    L, other = PromptLayer(X, k, T), PromptLayer(X, k, T)
+    r, y, logits = inputs(E, H, T, 6)
+    L.norm(r, y, T)
+    L.route(logits, T)
+    want = L.forward(T).clone()
+    assert L.error() == (0, 0)
+    with short_waits:
+        L.forward(T)
+    assert other.error() == (0, 0) and pm.grouped_error() == (0, 0)
+    assert L.error()[0] == 3
+    assert L.error() == (0, 0)
+    assert torch.equal(L.forward(T), want) and L.error() == (0, 0)

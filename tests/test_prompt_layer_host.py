@@ -80,3 +80,26 @@ def test_decoding_a_stored_layer_allocates_on_its_own_stream(monkeypatch):
     assert X.up.shape == (E, 2 * I, H)
     assert set(streams) == {"the given stream"} and len(streams) == 3 * E
     assert len(made) >= 4 and set(made) == {"the given stream"}
+
+
+def test_a_layer_has_a_record_of_its_own(calls, monkeypatch):
+    """Both products of a layer record a wait that ran out in the layer's own words, not in the device's that every
+    caller clears; the words are taken once."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    L, other = layer(1), layer(1)
+    L.forward(5)
+    made = {n: a for n, a in calls}
+    for name in ("grouped_swiglu", "grouped_matmul"):
+        assert made[name][1].error == L.errors.data_ptr() != other.errors.data_ptr()
+    assert L.error() == (0, 0)
+    L.errors[0], L.errors[1] = 3, 10
+    assert L.error() == (3, 10) and L.error() == (0, 0)
+
+
+def test_a_record_that_is_not_aligned_is_refused():
+    import bitplane_mixed_precision_b200 as pm
+    A = 1 << 20  # refused calls never follow it
+    with pytest.raises(pm.PmoeError) as ei:
+        pm.grouped_matmul(pm.make_dense(1, A, A, 4, 64, 256), pm.make_rows(1, A, A, 10, None, A + 4), A, 10, 2, A)
+    assert ei.value.code == 1
