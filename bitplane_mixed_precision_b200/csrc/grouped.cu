@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this fence
         if (g.index) {
             Ring<S::kStages> ring;
-            int left = t0 < tiles ? (tiles - t0 + step - 1) / step * g.iters : 0;
+            int64_t left = t0 < tiles ? (int64_t)((tiles - t0 - 1) / step + 1) * g.iters : 0;
             const bool leader = elect_one();
             for (; left > 0; --left, ring.next()) {
                 if (!warp_wait(wait, &bars->gathered[ring.s], ring.phase, 11))
@@ -875,7 +875,6 @@ pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offs
         return PMOE_ERR_UNSUPPORTED;
     if (rows == 0)
         return PMOE_OK;
-    PMOE_TRY(on_current_device({W->w, W->scales, X->x, X->scales, X->index, X->error, offsets, out, out_scales}));
 
     // Rows of x per tile by the rows an expert has on average: at 16, tiles of 32 against 128 took 181 against 176 us
     // (q8, 256 experts of 4096 x 1024), 177 against 187 (q8 SwiGLU), 333 against 339 (bf16); at 32, 227 against 182 and
@@ -888,9 +887,11 @@ pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offs
     const int nt = most * ((width + wide - 1) / wide) < kNumSMs / 2 ? 128 : 256;
     const int cols = swiglu ? nt / 2 : nt;
     const int ntiles = (width + cols - 1) / cols;
-    // offsets that overlap could name every row for every expert: even those tiles are counted in an int
-    if (((int64_t)rows + tile_rows - 1) / tile_rows * W->E * ntiles > INT32_MAX)
+    // offsets that overlap could name every row for every expert: even those tiles are counted in an int, which a role's
+    // last step past them must not leave; nor may the rows of a tile behind the last row
+    if (((int64_t)rows + tile_rows - 1) / tile_rows * W->E * ntiles > INT32_MAX - kNumSMs || rows > INT32_MAX - kLanes)
         return PMOE_ERR_UNSUPPORTED;
+    PMOE_TRY(on_current_device({W->w, W->scales, X->x, X->scales, X->index, X->error, offsets, out, out_scales}));
     const int elem = is_q8 ? 1 : 2;
     const uint64_t K = (uint64_t)W->K;
     Maps m{}; // no maps of x where it is gathered

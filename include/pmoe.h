@@ -670,8 +670,8 @@ typedef struct {
  *   16-byte aligned.
  *   The tensor cores add to their float sums by truncation: about 1e-6 of the
  *   result's norm at K = 1024, growing with K.
- *   PMOE_ERR_UNSUPPORTED: more than 2048 experts, or rows/32 * E * N/64 past
- *   2^31.
+ *   PMOE_ERR_UNSUPPORTED: more than 2048 experts, rows past 2^31 - 129, or
+ *   rows/32 * E * N/64 past 2^31 - 149.
  */
 PMOE_API pmoe_status pmoe_grouped_matmul(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offsets, int rows,
                                          int out_type, void *out, pmoe_stream stream);
