@@ -57,7 +57,6 @@ constexpr int kThreads = 256 + 32 * kGatherWarps + 32; // producer, MMA, two sca
 constexpr int kLanes = 128;                       // the MMA's M
 constexpr int kStageRowBytes = 128;               // epilogue staging: bytes per row
 constexpr uint64_t kDrainNs = 1000ull * 1000 * 1000;
-constexpr uint64_t kSettleNs = 5ull * 1000 * 1000; // hundreds of times what a load takes
 
 // A record of the first wait that ran out, {code 3, which}, as one word that is written and taken in one step. This one
 // is for calls without a record of their own, since pmoe_grouped_error last took it.
@@ -76,6 +75,7 @@ struct Grouped {
 };
 
 constexpr int kMostStages = 12;
+constexpr int64_t kNone = INT64_MAX;
 
 template <bool Q8IN, int ROWS, int NT> struct Shape {
     static constexpr int kA = kLanes * kRowBytes, kB = NT * kRowBytes;
@@ -113,6 +113,9 @@ struct Bars {
     uint32_t tmem;
     int abort;
     int part[kThreads / 32];
+    // stages that a role has arrived for when it finishes (kNone owed where it has no part)
+    int64_t full_by[4];               // producer, scale warps, hand-over
+    int64_t gathered_by[kGatherWarps];
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
 
@@ -177,10 +180,36 @@ __device__ void drain(uint64_t *bar, uint32_t parity)
     }
 }
 
+// After all roles have finished, some of them early: one thread waits for the copies that nobody waited for. They count
+// towards their stages' barriers, so it makes the arrivals that are owed there (`each` by an owner that stopped before
+// that stage). No owner is a whole turn of the ring ahead of another, so a barrier is at the phase of the last stage of
+// `end` that it belongs to, or behind it.
+template <int STAGES>
+__device__ void land(uint64_t *bars, int64_t end, const int64_t *stopped, int owners, uint32_t each, uint64_t deadline)
+{
+    for (int64_t n = end > STAGES ? end - STAGES : 0; n < end; ++n) {
+        uint64_t *bar = bars + n % STAGES;
+        uint32_t owed = 0;
+        for (int i = 0; i < owners; ++i)
+            owed += stopped[i] <= n ? each : 0;
+        if (owed)
+            asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(pipe::smem_u32(bar)), "r"(owed)
+                         : "memory");
+        while (!pipe::mbar_try_wait(bar, (uint32_t)(n / STAGES) & 1) && pipe::globaltimer() < deadline) {
+        }
+    }
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float a, float b)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Stages of this CTA's tiles t0, t0 + step, ... before tile t.
+__device__ __forceinline__ int64_t stages_before(const Grouped &g, int t, int t0, int step)
+{
+    return (int64_t)((t - t0) / step) * g.iters;
 }
 
 // The ring's stages in order: stage s for the (phase)th time.
@@ -326,9 +355,11 @@ __device__ __forceinline__ bool epilogue_all(bool ok)
 // loaded together, while those of the four before are handed over. (Two or three such groups ahead, or a loop
 // unrolled over them, were 1 to 8 % slower.) rows_of(T, j) is the row's scale bytes, or NULL where
 // the values are zeros or not used (scale 1, so that zeros stay zeros).
+// Returns the stages it arrived for.
 template <class S, int ROWS, class RowsOf, class Tiles>
-__device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const Waiter &wait, uint8_t *dst, int tiles,
-                                           int t0, int step, int where, const RowsOf &rows_of, Tiles tile)
+__device__ __forceinline__ int64_t scale_warp(const Grouped &g, Bars *bars, const Waiter &wait, uint8_t *dst,
+                                              int tiles, int t0, int step, int where, const RowsOf &rows_of,
+                                              Tiles tile)
 {
     const int lane = threadIdx.x & 31;
     const int groups = (g.iters + 3) / 4;
@@ -369,7 +400,8 @@ __device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const W
     };
     load();
     Ring<S::kStages> ring;
-    for (int t = t0; t < tiles; t += step) {
+    int t = t0;
+    for (; t < tiles; t += step) {
         for (int k = 0; k < g.iters; k += 4) {
             uint4 now[ROWS];
 #pragma unroll
@@ -381,7 +413,7 @@ __device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const W
                 if (k + q >= g.iters)
                     break;
                 if (!ring.free(wait, bars, where))
-                    return;
+                    return stages_before(g, t, t0, step) + k + q;
                 auto word = [&](int j) {
                     return j >= ROWS ? kOnes : q == 0 ? now[j].x : q == 1 ? now[j].y : q == 2 ? now[j].z : now[j].w;
                 };
@@ -397,6 +429,7 @@ __device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const W
             }
         }
     }
+    return stages_before(g, t, t0, step);
 }
 
 template <bool Q8IN, bool SWIGLU, int ROWS, int NT, int OUT>
@@ -457,12 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- producer
         const bool leader = elect_one();
         Ring<S::kStages> ring;
-        for (int t = t0; t < tiles; t += step) {
+        int t = t0, i = 0;
+        for (; t < tiles; t += step) {
             const Tile T = tile(t);
             const bool one = ROWS == 128 && T.rows > 64; // one box of 128 rows
             const int loads = g.index ? 0 : one ? 1 : (T.rows + 31) / 32;
             const uint32_t bytes = (uint32_t)(loads * (one ? 128 : 32) * kRowBytes + S::kB);
-            for (int i = 0; i < g.iters; ++i, ring.next()) {
+            for (i = 0; i < g.iters; ++i, ring.next()) {
                 const int s = ring.s;
                 if (!ring.free(wait, bars, 1))
                     goto produced;
@@ -479,8 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
+            i = 0;
         }
     produced:
+        if (lane == 0)
+            bars->full_by[0] = stages_before(g, t, t0, step) + i;
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA: the warp goes through the stages together, one lane issues
@@ -538,8 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 2) {
         // ---- scale bytes of the rows of x
+        int64_t arrived = kNone;
         if (Q8IN)
-            scale_warp<S, ROWS / 32>(
+            arrived = scale_warp<S, ROWS / 32>(
                 g, bars, wait, smem + S::kScalesAt, tiles, t0, step, 6,
                 [&](const Tile &T, int r) -> const uint8_t * {
                     if (r >= T.rows)
@@ -548,11 +586,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return (uint32_t)i < (uint32_t)g.n ? g.xs + (int64_t)i * (g.K / 32) : nullptr;
                 },
                 tile);
+        if (lane == 0)
+            bars->full_by[1] = arrived;
         __syncwarp();
     } else if (warp == 3) {
         // ---- scale bytes of the matrix rows
+        int64_t arrived = kNone;
         if (Q8IN)
-            scale_warp<S, NT / 32>(
+            arrived = scale_warp<S, NT / 32>(
                 g, bars, wait, smem + S::kScalesAt + 512, tiles, t0, step, 7,
                 [&](const Tile &T, int r) -> const uint8_t * {
                     const bool up = SWIGLU && (r & 32);
@@ -560,15 +601,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return c < g.width ? g.ws + ((int64_t)T.e * g.N + c + (up ? g.width : 0)) * (g.K / 32) : nullptr;
                 },
                 tile);
+        if (lane == 0)
+            bars->full_by[2] = arrived;
         __syncwarp();
     } else if (warp == 8 + kGatherWarps) {
         // ---- hands gathered rows over: the copies land as other threads' writes, which the tensor cores see behind
         // this fence
+        int64_t n = kNone;
         if (g.index) {
             Ring<S::kStages> ring;
-            int64_t left = t0 < tiles ? (int64_t)((tiles - t0 - 1) / step + 1) * g.iters : 0;
+            const int64_t all = t0 < tiles ? (int64_t)((tiles - t0 - 1) / step + 1) * g.iters : 0;
             const bool leader = elect_one();
-            for (; left > 0; --left, ring.next()) {
+            for (n = 0; n < all; ++n, ring.next()) {
                 if (!warp_wait(wait, &bars->gathered[ring.s], ring.phase, 11))
                     break;
                 if (leader) {
@@ -578,6 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
         }
+        if (lane == 0)
+            bars->full_by[3] = n;
         __syncwarp();
     } else if (warp >= 8) {
         // ---- gathered rows of x: a thread has one 16-byte chunk of rows r0, r0 + 16, ...
@@ -586,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t pitch = (int64_t)g.K * kElem;
             const uint32_t at = (uint32_t)(r0 * kRowBytes + ((chunk ^ (r0 & 7)) << 4)); // 16 more rows: 2 KB more
             Ring<S::kStages> ring;
-            for (int t = t0; t < tiles; t += step) {
+            int t = t0, i = 0;
+            for (; t < tiles; t += step) {
                 const Tile T = tile(t);
                 const uint8_t *src[ROWS / 16];
                 uint32_t live = 0; // rows inside x
@@ -595,14 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int r = r0 + 16 * j;
                     src[j] = g.x + 16 * chunk;
                     if (r < T.rows) {
-                        const int i = __ldg(g.index + T.row0 + r);
-                        if ((uint32_t)i < (uint32_t)g.n) {
-                            src[j] += i * pitch;
+                        const int from = __ldg(g.index + T.row0 + r);
+                        if ((uint32_t)from < (uint32_t)g.n) {
+                            src[j] += from * pitch;
                             live |= 1u << j;
                         }
                     }
                 }
-                for (int i = 0; i < g.iters; ++i, ring.next()) {
+                for (i = 0; i < g.iters; ++i, ring.next()) {
                     if (!ring.free(wait, bars, 9))
                         goto gathered;
                     const uint32_t dst = pipe::smem_u32(smem + ring.s * (S::kA + S::kB)) + at;
@@ -616,9 +663,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             copy16(dst + j * 16 * kRowBytes, src[j] + off, in && (live >> j & 1) ? 16 : 0);
                     copies_arrive(&bars->gathered[ring.s]);
                 }
+                i = 0;
             }
         gathered:
             asm volatile("cp.async.wait_all;" ::: "memory");
+            if (lane == 0)
+                bars->gathered_by[warp - 8] = stages_before(g, t, t0, step) + i;
             __syncwarp();
         }
     } else if (ROWS == 32) {
@@ -793,15 +843,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
-    if (*reinterpret_cast<volatile int *>(&bars->abort)) // loads that nobody waited for land meanwhile
-        for (const uint64_t until = pipe::globaltimer() + kSettleNs; pipe::globaltimer() < until;) {
-        }
-    __syncwarp();
     umma::fence_before_sync();
     __syncthreads();
     if (warp == 1) {
         umma::fence_after_sync();
         umma::tmem_dealloc(tmem, S::kTmemCols);
+    }
+    if (threadIdx.x == 0 && bars->abort) {
+        const uint64_t deadline = pipe::globaltimer() + kDrainNs;
+        land<S::kStages>(bars->full, bars->full_by[0], bars->full_by, 4, 1, deadline);
+        if (g.index) {
+            int64_t end = 0;
+            for (int i = 0; i < kGatherWarps; ++i)
+                end = max(end, bars->gathered_by[i]);
+            land<S::kStages>(bars->gathered, end, bars->gathered_by, kGatherWarps, 32, deadline);
+        }
     }
 }
 

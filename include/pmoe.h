@@ -360,7 +360,8 @@ PMOE_API pmoe_status pmoe_layer_error(const void *ws, int *code, int *detail, pm
  * kernel's own copies to land before it exits have a separate bound, 200 ms
  * past that one.
  * In the grouped products the limit counts from the start of each wait (see
- * pmoe_grouped_error).
+ * pmoe_grouped_error), and waits for their own copies and MMAs to land after
+ * one that ran out are bounded by 1 s.
  * 0 restores the default of 200 ms. Host only; the kernels stay correct with
  * any limit that is not reached.
  */

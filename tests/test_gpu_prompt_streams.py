@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from bitplane_mixed_precision_b200.prompt import DenseExperts, PromptLayer
+from prompt_common import quantize
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +170,69 @@ def test_a_layer_reports_a_wait_that_ran_out(pm, short_waits, kind):
     assert L.error()[0] == 3
     assert L.error() == (0, 0)
     assert torch.equal(L.forward(T), want) and L.error() == (0, 0)
+
+
+def test_a_product_that_gives_up_ends_once_its_own_copies_have_landed(pm, short_waits):
+    """No fixed pause is put in their place: a call that gives up in its first tile takes less than a complete one and
+    2 ms beside."""
+    a = Product(pm, 7)
+
+    def timed():
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        start.record(torch.cuda.default_stream())
+        a(pm, True)
+        end.record(torch.cuda.default_stream())
+        torch.cuda.synchronize()
+        return start.elapsed_time(end)
+
+    timed()
+    full = min(timed() for _ in range(3))
+    with short_waits:
+        short = min(timed() for _ in range(3))
+    assert a.error.tolist()[0] == 3
+    assert short <= full + 2.0, (short, full)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("rows", [20, 700])
+def test_products_that_give_up_at_different_places(pm, kind, gather, rows):
+    """Limits from 1 ns to some 50 us stop the roles at different stages; calls follow one another at once on the same
+    SMs, and the first call with the default limit is exact again."""
+    g = gen(8)
+    E, K, N = 3, 4096, 1024
+    M, n = E * rows, 100 if gather else E * rows
+    t = pm.Q8 if kind == "q8" else pm.BF16
+    x, w = torch.randn(n, K, generator=g, device="cuda"), torch.randn(E, N, K, generator=g, device="cuda")
+    xs = ws = None
+    if kind == "q8":
+        (x, xs), (w, ws) = quantize(x), quantize(w)
+    else:
+        x, w = x.bfloat16(), w.bfloat16()
+    index = torch.randint(0, n, (M,), generator=g, device="cuda").to(torch.int32) if gather else None
+    offsets = torch.tensor([0, rows, 2 * rows, M], dtype=torch.int32, device="cuda")
+    error = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out = torch.empty(M, N, device="cuda")
+    dense, x_rows = pm.make_dense(t, w, ws, E, N, K), pm.make_rows(t, x, xs, n, index, error)
+
+    def call():
+        pm.grouped_matmul(dense, x_rows, offsets, M, pm.F32, out)
+
+    call()
+    torch.cuda.synchronize()
+    want = out.clone()
+    assert error.tolist() == [0, 0]
+    try:
+        for ns in (1, 600, 2000, 5000, 10000, 20000, 50000):
+            pm.set_wait_limit_ns(ns)
+            for _ in range(20):
+                call()
+    finally:
+        torch.cuda.synchronize()
+        pm.set_wait_limit_ns(0)
+    error.zero_()
+    out.zero_()
+    call()
+    torch.cuda.synchronize()
+    assert error.tolist() == [0, 0] and torch.equal(out, want)
