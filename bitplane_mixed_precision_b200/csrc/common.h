@@ -25,7 +25,8 @@ inline pmoe_status launch_status() { return cuda_status(cudaGetLastError()); }
 
 // Launches a kernel that may start before the launch in front of it on the stream has finished, up to its
 // pipe::wait_prerequisites(): its setup then overlaps that one's end. Every such kernel calls that before it touches
-// global memory.
+// global memory, and reads by plain loads: what the launch in front writes is not read-only while this one is resident,
+// which is what __ldg, and a pointer that is const and __restrict__, would promise.
 template <class... P, class... A>
 pmoe_status launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args)
 {

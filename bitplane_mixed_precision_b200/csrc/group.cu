@@ -25,8 +25,8 @@ inline int group_blocks(int64_t P)
     return (int)(b < 1 ? 1 : b < kNumSMs ? b : kNumSMs);
 }
 
-__global__ void __launch_bounds__(kGroupThreads) group_histogram_kernel(const int32_t *__restrict__ ids, int P, int E,
-                                                                        int chunk, int32_t *__restrict__ hist)
+__global__ void __launch_bounds__(kGroupThreads) group_histogram_kernel(const int32_t *ids, int P, int E, int chunk,
+                                                                        int32_t *__restrict__ hist)
 {
     extern __shared__ int32_t h[];
     for (int e = threadIdx.x; e < E; e += kGroupThreads)
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_histogram_kernel(const in
     const int p0 = blockIdx.x * chunk, p1 = min(P - p0, chunk) + p0;
 #pragma unroll 8
     for (int p = p0 + threadIdx.x; p < p1; p += kGroupThreads) {
-        const uint32_t e = (uint32_t)__ldg(ids + p);
+        const uint32_t e = (uint32_t)ids[p];
         if (e < (uint32_t)E)
             atomicAdd(&h[e], 1); // whole numbers: the order does not show
     }
@@ -55,7 +55,7 @@ __device__ __forceinline__ void load_batches(const int32_t *ids, int p, int end,
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
-        id[j] = p + 32 * j + lane < end ? (uint32_t)__ldg(ids + p + 32 * j + lane) : 0xffffffffu;
+        id[j] = p + 32 * j + lane < end ? (uint32_t)ids[p + 32 * j + lane] : 0xffffffffu;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
         id[j] = id[j] < (uint32_t)E ? id[j] : 0xffffffffu;
@@ -81,9 +81,8 @@ __device__ __forceinline__ void load_batches(const int32_t *ids, int p, int end,
 // warp, 32 pairs at a time, the lanes before with the same expert. hist (one row per block) is NULL when
 // one block has all pairs.
 __global__ void __launch_bounds__(kGroupThreads)
-    group_scatter_kernel(const int32_t *__restrict__ ids, int P, int k, int E, int chunk,
-                         const int32_t *__restrict__ hist, int32_t *__restrict__ offsets,
-                         int32_t *__restrict__ row_of, int32_t *__restrict__ token_of)
+    group_scatter_kernel(const int32_t *ids, int P, int k, int E, int chunk, const int32_t *hist,
+                         int32_t *__restrict__ offsets, int32_t *__restrict__ row_of, int32_t *__restrict__ token_of)
 {
     extern __shared__ int32_t cnt[]; // [kGroupWarps][E]
     __shared__ int32_t scan[kGroupWarps];
@@ -127,7 +126,7 @@ __global__ void __launch_bounds__(kGroupThreads)
                     int32_t n[20];
 #pragma unroll
                     for (int j = 0; j < 20; ++j)
-                        n[j] = b0 + j < (int)gridDim.x ? __ldg(hist + (int64_t)(b0 + j) * E + e) : 0;
+                        n[j] = b0 + j < (int)gridDim.x ? hist[(int64_t)(b0 + j) * E + e] : 0;
 #pragma unroll
                     for (int j = 0; j < 20; ++j) {
                         total += n[j];
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(kGroupThreads)
 __device__ __forceinline__ void load8(const void *rows, int64_t at, float (&v)[8], bool bf16)
 {
     if (bf16) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(rows) + at));
+        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(rows) + at);
         const uint32_t q[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -207,7 +206,7 @@ __device__ __forceinline__ void load8(const void *rows, int64_t at, float (&v)[8
         }
     } else {
         const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(rows) + at);
-        const float4 a = __ldg(f), b = __ldg(f + 1);
+        const float4 a = f[0], b = f[1];
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
         v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
@@ -217,8 +216,7 @@ __device__ __forceinline__ void load8(const void *rows, int64_t at, float (&v)[8
 // 4096 tokens of 10 bf16 rows of 4096 take 66 us, 5.8 TB/s of what has to be read and written.
 template <bool BF16>
 __global__ void __launch_bounds__(128)
-    combine_rows_kernel(const void *__restrict__ rows, const int32_t *__restrict__ row_of, const float *__restrict__ w,
-                        int P, int k, int H, int chunks, float *__restrict__ y)
+    combine_rows_kernel(const void *rows, const int32_t *row_of, const float *w, int P, int k, int H, int chunks, float *__restrict__ y)
 {
     const int t = blockIdx.x / chunks;
     const int c = 8 * ((blockIdx.x % chunks) * 128 + threadIdx.x);
@@ -229,10 +227,10 @@ __global__ void __launch_bounds__(128)
     pipe::wait_prerequisites();
 #pragma unroll 4
     for (int i = 0; i < k; ++i) {
-        const int row = __ldg(row_of + (int64_t)t * k + i);
+        const int row = row_of[(int64_t)t * k + i];
         if ((uint32_t)row >= (uint32_t)P)
             continue;
-        const float wt = __ldg(w + (int64_t)t * k + i);
+        const float wt = w[(int64_t)t * k + i];
         float v[8];
         load8(rows, (int64_t)row * H + c, v, BF16);
 #pragma unroll

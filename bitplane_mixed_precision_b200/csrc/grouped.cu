@@ -238,7 +238,7 @@ struct Tile {
 // Rows of expert e as far as `offsets` is sound: [first, last) within [0, rows).
 __device__ __forceinline__ int2 expert_rows(const Grouped &g, int e)
 {
-    const int a = max(0, __ldg(g.offsets + e)), b = min(g.rows, __ldg(g.offsets + e + 1));
+    const int a = max(0, g.offsets[e]), b = min(g.rows, g.offsets[e + 1]);
     return make_int2(a, max(a, b));
 }
 
@@ -383,13 +383,13 @@ __device__ __forceinline__ int64_t scale_warp(const Grouped &g, Bars *bars, cons
             if (row[j]) {
                 const uint32_t *p = reinterpret_cast<const uint32_t *>(row[j]) + 4 * group;
                 if (wide) {
-                    next[j] = __ldg(reinterpret_cast<const uint4 *>(p));
+                    next[j] = *reinterpret_cast<const uint4 *>(p);
                 } else {
                     const int left = g.iters - 4 * group;
-                    next[j].x = __ldg(p);
-                    next[j].y = left > 1 ? __ldg(p + 1) : kOnes;
-                    next[j].z = left > 2 ? __ldg(p + 2) : kOnes;
-                    next[j].w = left > 3 ? __ldg(p + 3) : kOnes;
+                    next[j].x = p[0];
+                    next[j].y = left > 1 ? p[1] : kOnes;
+                    next[j].z = left > 2 ? p[2] : kOnes;
+                    next[j].w = left > 3 ? p[3] : kOnes;
                 }
             }
         }
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 [&](const Tile &T, int r) -> const uint8_t * {
                     if (r >= T.rows)
                         return nullptr;
-                    const int i = g.index ? __ldg(g.index + T.row0 + r) : T.row0 + r;
+                    const int i = g.index ? g.index[T.row0 + r] : T.row0 + r;
                     return (uint32_t)i < (uint32_t)g.n ? g.xs + (int64_t)i * (g.K / 32) : nullptr;
                 },
                 tile);
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int r = r0 + 16 * j;
                     src[j] = g.x + 16 * chunk;
                     if (r < T.rows) {
-                        const int from = __ldg(g.index + T.row0 + r);
+                        const int from = g.index[T.row0 + r];
                         if ((uint32_t)from < (uint32_t)g.n) {
                             src[j] += from * pitch;
                             live |= 1u << j;

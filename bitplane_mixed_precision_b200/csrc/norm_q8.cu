@@ -24,8 +24,7 @@ __device__ __forceinline__ uint2 bf16x4(float4 v)
 // as streams, which leaves its room to the codes that the next call reads: 37.9 us against 38.8).
 template <int V>
 __global__ void __launch_bounds__(kMaxNormThreads)
-    residual_norm_q8_kernel(float *__restrict__ r, const float *__restrict__ y, const float *__restrict__ gain,
-                            float eps, int H, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+    residual_norm_q8_kernel(float *__restrict__ r, const float *y, const float *gain, float eps, int H, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                             uint16_t *__restrict__ x)
 {
     __shared__ float part[32];
@@ -79,7 +78,7 @@ __global__ void __launch_bounds__(kMaxNormThreads)
             break;
         float4 o = make_float4(v[j].x * inv, v[j].y * inv, v[j].z * inv, v[j].w * inv);
         if (gain != nullptr) {
-            const float4 g = __ldg(reinterpret_cast<const float4 *>(gain + 4 * i));
+            const float4 g = *reinterpret_cast<const float4 *>(gain + 4 * i);
             o = make_float4(o.x * g.x, o.y * g.y, o.z * g.z, o.w * g.w);
         }
         if (x != nullptr)
@@ -97,8 +96,8 @@ __global__ void __launch_bounds__(kMaxNormThreads)
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(256) quantize_q8_kernel(const void *__restrict__ w, int64_t n4,
-                                                          uint8_t *__restrict__ codes, uint8_t *__restrict__ scales)
+__global__ void __launch_bounds__(256) quantize_q8_kernel(const void *w, int64_t n4, uint8_t *__restrict__ codes,
+                                                          uint8_t *__restrict__ scales)
 {
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
     pipe::launch_dependents();
@@ -108,11 +107,11 @@ __global__ void __launch_bounds__(256) quantize_q8_kernel(const void *__restrict
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (i < n4) {
             if (BF16) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(w) + i);
+                const uint2 u = reinterpret_cast<const uint2 *>(w)[i];
                 o = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
                                 __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
             } else {
-                o = __ldg(reinterpret_cast<const float4 *>(w) + i);
+                o = reinterpret_cast<const float4 *>(w)[i];
             }
         }
         const uint32_t byte = q8::scale_byte(q8::top_of_8_lanes(q8::top4(o.x, o.y, o.z, o.w)));

@@ -236,3 +236,82 @@ def test_products_that_give_up_at_different_places(pm, kind, gather, rows):
     call()
     torch.cuda.synchronize()
     assert error.tolist() == [0, 0] and torch.equal(out, want)
+
+
+# ---------------------------------------------------------------- one launch behind another
+
+def test_pairs_again_in_one_workspace(pm):
+    """Calls at once behind one another, with other ids and outputs but the same workspace, captured too: a call's
+    histograms are not written before the sort in front has read its own."""
+    T, k, E, n = 2000, 5, 300, 12
+    P = T * k
+    sets = [torch.randint(-1, E, (T, k), dtype=torch.int32, generator=gen(30 + i), device="cuda") for i in range(n)]
+    size = pm.group_workspace_bytes(T, k, E)
+    assert size > 0  # several blocks
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def outputs():
+        return [[torch.full((m,), -7, dtype=torch.int32, device="cuda") for m in (E + 1, P, P)] for _ in range(n)]
+
+    def run(outs, pause):
+        for ids, o in zip(sets, outs):
+            pm.group_pairs(ids, T, k, E, *o, ws, size, torch.cuda.current_stream())
+            if pause:
+                torch.cuda.synchronize()
+
+    want, got, replayed = outputs(), outputs(), outputs()
+    run(want, True)
+    for ids, (offsets, row_of, _) in zip(sets, want):
+        flat = torch.where(ids.reshape(-1) < 0, E, ids.reshape(-1)).long()
+        assert torch.equal(offsets[1:], torch.bincount(flat, minlength=E + 1)[:E].cumsum(0).int())
+        order = torch.argsort(flat, stable=True)[: int(offsets[-1])]
+        assert torch.equal(row_of[order], torch.arange(order.numel(), dtype=torch.int32, device="cuda"))
+    for _ in range(3):
+        run(got, False)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(replayed, False)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for w, a, b in zip(want, got, replayed):
+        assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(w, a, b))
+
+
+@pytest.mark.parametrize("T", [3, 600])
+@pytest.mark.parametrize("kind", [0, 1])
+def test_a_layer_again_and_again_in_the_same_buffers(pm, kind, T):
+    """Nothing but the layer's own launches, each of which may start while the one in front still writes what it reads;
+    two sets of ids take turns, so that every buffer holds another call's values first."""
+    E, H, I, k, n = 40, 512, 256, 4, 16
+    X = experts(kind, E, H, I, 9)
+    L, P = PromptLayer(X, k, T), T * k
+    ids = [torch.randint(-1, E, (T, k), dtype=torch.int32, generator=gen(40 + i), device="cuda") for i in range(2)]
+    r0 = torch.randn(T, H, generator=gen(42), device="cuda")
+    L.w.copy_(torch.rand(T, k, generator=gen(43), device="cuda"))
+    sums = [torch.empty(T, H, device="cuda") for _ in range(n)]
+
+    def run(pause):
+        r, y = r0.clone(), None
+        steps = []
+        for i in range(n):
+            steps += [lambda y=y: L.norm(r, y, T), lambda i=i: pm.group_pairs(
+                          ids[i % 2], T, k, E, L.offsets, L.row_of, L.token_of, L.ws, L.ws.numel(), st),
+                      lambda: pm.grouped_swiglu(X.up_dense, pm.make_rows(kind, L.x, L.x_scales, T, L.token_of),
+                                                L.offsets, P, kind, L.h, L.h_scales, st),
+                      lambda: pm.grouped_matmul(X.down_dense, pm.make_rows(kind, L.h, L.h_scales, P), L.offsets, P,
+                                                pm.BF16, L.out, st),
+                      lambda i=i: pm.combine_rows(L.out, True, L.row_of, L.w, T, k, H, sums[i], st)]
+            y = sums[i]
+        st = torch.cuda.current_stream()
+        for s in steps:
+            s()
+            if pause:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [r] + [s.clone() for s in sums]
+
+    want = run(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
+    assert float(want[0].abs().max()) < float("inf") and pm.grouped_error() == (0, 0)
