@@ -2,6 +2,8 @@
 // conversion of rows to q8.
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "common.h"
 #include "pipe.cuh"
 #include "q8.cuh"
@@ -18,6 +20,47 @@ __device__ __forceinline__ uint2 bf16x4(float4 v)
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
+// The block's largest value (as bits of a magnitude, so that a NaN is the largest); all threads.
+__device__ __forceinline__ uint32_t block_top(uint32_t top, uint32_t *part)
+{
+    const int lane = threadIdx.x & 31;
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0)
+        part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? part[lane] : 0u);
+}
+
+// The block's sum, in a fixed order; all threads.
+__device__ __forceinline__ float block_sum(float s, float *part)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0)
+        part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, d);
+    return s;
+}
+
+template <int V> __device__ __forceinline__ float squares(const float4 (&v)[V])
+{
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        ss = fmaf(v[j].x, v[j].x, ss);
+        ss = fmaf(v[j].y, v[j].y, ss);
+        ss = fmaf(v[j].z, v[j].z, ss);
+        ss = fmaf(v[j].w, v[j].w, ss);
+    }
+    return ss;
+}
+
 // One block per token, V float4 of the row per thread, held in registers between the sum of squares and
 // the output: r and y are read once and r written once. 8 neighbouring lanes hold one 32-column block. Bound by memory:
 // 4096 x 4096 takes 38 us, 5.8 TB/s of the 13 bytes an element that have to move (with r and y passed through the L2
@@ -27,11 +70,11 @@ __global__ void __launch_bounds__(kMaxNormThreads)
     residual_norm_q8_kernel(float *__restrict__ r, const float *y, const float *gain, float eps, int H, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                             uint16_t *__restrict__ x)
 {
-    __shared__ float part[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n4 = H / 4;
+    __shared__ float part[32], sums[32];
+    __shared__ uint32_t tops[32];
+    const int tid = threadIdx.x, lane = tid & 31, n4 = H / 4;
     const int64_t row = (int64_t)blockIdx.x * H;
     float4 v[V];
-    float ss = 0.0f;
     pipe::launch_dependents();
     pipe::wait_prerequisites();
 #pragma unroll
@@ -54,23 +97,30 @@ __global__ void __launch_bounds__(kMaxNormThreads)
         const int i = tid + j * blockDim.x;
         if (y != nullptr && i < n4)
             __stcs(reinterpret_cast<float4 *>(r + row + 4 * i), v[j]);
-        ss = fmaf(v[j].x, v[j].x, ss);
-        ss = fmaf(v[j].y, v[j].y, ss);
-        ss = fmaf(v[j].z, v[j].z, ss);
-        ss = fmaf(v[j].w, v[j].w, ss);
     }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1)
-        ss += __shfl_xor_sync(0xffffffffu, ss, s);
-    if (lane == 0)
-        part[warp] = ss;
-    __syncthreads();
-    float all = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1)
-        all += __shfl_xor_sync(0xffffffffu, all, s);
+    const float all = block_sum(squares(v), part);
     const float ms = all / (float)H + eps;
-    const float inv = ms == 0.0f ? 0.0f : 1.0f / sqrtf(ms);
+    float inv = ms == 0.0f ? 0.0f : 1.0f / sqrtf(ms);
+    // Where squares of finite values leave the floats, or what underflowed of them (2^-150 each) is not far below the
+    // rest, the row is multiplied by a power of two first, which brings its largest magnitude to 1..2, or eps to at most
+    // 2 where that comes first. The whole block takes this path or not.
+    if (!(all <= FLT_MAX) || all + (float)H * eps < 0x1p-100f) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            top = max(top, q8::top4(v[j].x, v[j].y, v[j].z, v[j].w));
+        top = block_top(top, tops);
+        if (top < 0x7f800000u && top != 0u) {
+            int up = max(-126, 127 - (int)(top >> 23));
+            if (eps > 0.0f)
+                up = min(up, (128 - (int)(__float_as_uint(eps) >> 23)) / 2);
+            const float by = __uint_as_float((uint32_t)(up + 127) << 23);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] = make_float4(v[j].x * by, v[j].y * by, v[j].z * by, v[j].w * by);
+            inv = 1.0f / sqrtf(block_sum(squares(v), sums) / (float)H + by * eps * by);
+        }
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int i = tid + j * blockDim.x;

@@ -612,7 +612,9 @@ PMOE_API pmoe_status pmoe_quantize_q8(const void *w, int w_is_bf16, int64_t rows
  * bits. Per token t: r_t += y_t (skipped when y is NULL), then
  *   v_t = r_t * inv_t * gain,  inv_t = 1 / sqrt(mean of r_t^2 + eps)
  * (inv_t = 0 where that root is 0; gain NULL = ones), stored as q8 and, when
- * x is given, also as bf16(v_t). Sums in float, in a fixed order.
+ * x is given, also as bf16(v_t). Sums in float, in a fixed order; a row of
+ * finite values whose squares leave the floats is scaled by a power of two
+ * first. (Rows with an infinity: inv_t = 0.)
  *   r: device float [T*H] (updated). y: device float [T*H] or NULL. gain:
  *   device float [H] or NULL. eps >= 0. codes: device uint8 [T][H], scales:
  *   device uint8 [T][H/32] (both or neither NULL; NULL only with x). x:

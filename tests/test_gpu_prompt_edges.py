@@ -4,6 +4,7 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
@@ -94,3 +95,68 @@ def test_group_pairs_where_its_counters_fill_48_kb(E):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     run = subprocess.run([sys.executable, "-c", COUNTERS, str(E)], cwd=root, capture_output=True, text=True, timeout=120)
     assert run.returncode == 0, run.stderr
+
+
+# ---------------------------------------------------------------- norm
+
+def norm_formula(r, gain, eps):
+    """(v, bound) in 64 bits: as test_gpu_prompt's, and a step of the subnormals, to which small values are rounded."""
+    r64 = r.double()
+    ms = r64.pow(2).mean(1, keepdim=True) + eps
+    v = torch.where(ms == 0, 0.0, r64 / ms.sqrt()) * gain.double()
+    return v, 30 * U * v.abs() + 2.0 ** -149 * (1 + gain.double().abs())
+
+
+@pytest.mark.parametrize("H", [128, 4096, 12800])
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-20, 1e-6])
+@pytest.mark.parametrize("scale", [1e-44, 1e-38, 1e-25, 1e-21, 1e-16, 1e-10, 1e10, 1e17, 1e18, 1e25, 5e37])
+def test_residual_norm_q8_over_the_floats(pm, scale, eps, H):
+    """Rows whose squares leave the floats at either end, one with a single large value, one of zeros; an eps that
+    counts beside them or does not."""
+    T = 4
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H)
+    r = torch.randn(T, H, generator=g, device="cuda").clamp(-6, 6) * scale
+    r[1, 1:] *= 1e-3
+    r[2] = 0.0
+    gain = 1 + 0.2 * torch.randn(H, generator=g, device="cuda")
+    eps = float(np.float32(eps))
+    v, dv = norm_formula(r, gain, eps)
+    before = r.clone()
+    codes, scales, x = empty(T, H), empty(T, H // 32), empty(T, H, dtype=torch.bfloat16)
+    pm.residual_norm_q8(r, None, gain, eps, T, H, codes, scales, x)
+    torch.cuda.synchronize()
+    assert torch.equal(r, before)
+    check_q8(codes, scales, v, dv)
+    check_near(x, v, dv, 2.0 ** -8)
+
+
+def test_residual_norm_q8_adds_before_it_scales(pm):
+    """The stored sum is r + y at both ends, and the norm is of that."""
+    T, H = 3, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    scale = torch.tensor([[1e-30], [1.0], [1e30]], device="cuda")
+    r, y = (torch.randn(T, H, generator=g, device="cuda") * scale for _ in range(2))
+    want = r + y
+    x = empty(T, H, dtype=torch.bfloat16)
+    pm.residual_norm_q8(r, y, None, 0.0, T, H, None, None, x)
+    torch.cuda.synchronize()
+    assert torch.equal(r, want)
+    v, dv = norm_formula(want, torch.ones(H, device="cuda"), 0.0)
+    check_near(x, v, dv, 2.0 ** -8)
+
+
+def test_residual_norm_q8_of_infinities(pm):
+    """As the formula has it in floats: the mean is infinite, its inverse root 0, so that finite values are zeros and
+    the infinite ones NaN."""
+    T, H = 2, 256
+    r = torch.ones(T, H, device="cuda")
+    r[0, 5], r[1, 200] = float("inf"), float("-inf")
+    codes, scales, x = empty(T, H), empty(T, H // 32), empty(T, H, dtype=torch.bfloat16)
+    pm.residual_norm_q8(r, None, None, 0.0, T, H, codes, scales, x)
+    torch.cuda.synchronize()
+    bad = r.isinf()
+    assert torch.equal(x.isnan(), bad) and not x[~bad].any()
+    blocks = bad.view(T, -1, 32).any(2)
+    assert torch.equal(scales == 255, blocks) and not scales[~blocks].any()
