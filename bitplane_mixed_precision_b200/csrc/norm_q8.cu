@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kMaxNormThreads)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int i = tid + j * blockDim.x;
-        if (i >= n4) // H % 128 == 0: whole warps
+        if (i >= n4) // whole warps where codes are made: H % 128 == 0
             break;
         float4 o = make_float4(v[j].x * inv, v[j].y * inv, v[j].z * inv, v[j].w * inv);
         if (gain != nullptr) {
@@ -199,7 +199,7 @@ pmoe_status pmoe_quantize_q8(const void *w, int w_is_bf16, int64_t rows, int K, 
 pmoe_status pmoe_residual_norm_q8(float *r, const float *y, const float *gain, float eps, int T, int H, uint8_t *codes,
                                   uint8_t *scales, uint16_t *x, pmoe_stream stream)
 {
-    if (!r || T < 0 || H <= 0 || H % 128 || !(eps >= 0.0f) || (!codes != !scales) || (!codes && !x) ||
+    if (!r || T < 0 || H <= 0 || H % (codes ? 128 : 8) || !(eps >= 0.0f) || (!codes != !scales) || (!codes && !x) ||
         !aligned(r, 16) || !aligned(y, 16) || !aligned(gain, 16) || !aligned(codes, 16) || !aligned(scales, 4) ||
         !aligned(x, 16))
         return PMOE_ERR_INVALID_ARG;

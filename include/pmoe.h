@@ -619,7 +619,8 @@ PMOE_API pmoe_status pmoe_quantize_q8(const void *w, int w_is_bf16, int64_t rows
  *   device float [H] or NULL. eps >= 0. codes: device uint8 [T][H], scales:
  *   device uint8 [T][H/32] (both or neither NULL; NULL only with x). x:
  *   device bf16 [T*H] or NULL. Pointers 16-byte aligned (scales: 4).
- *   H % 128 == 0, H <= 32768 (else PMOE_ERR_UNSUPPORTED).
+ *   H % 128 == 0 (with x alone: H % 8 == 0), H <= 32768 (else
+ *   PMOE_ERR_UNSUPPORTED).
  */
 PMOE_API pmoe_status pmoe_residual_norm_q8(float *r, const float *y, const float *gain, float eps, int T, int H,
                                            uint8_t *codes, uint8_t *scales, uint16_t *x, pmoe_stream stream);

@@ -160,3 +160,43 @@ def test_residual_norm_q8_of_infinities(pm):
     assert torch.equal(x.isnan(), bad) and not x[~bad].any()
     blocks = bad.view(T, -1, 32).any(2)
     assert torch.equal(scales == 255, blocks) and not scales[~blocks].any()
+
+
+@pytest.mark.parametrize("T,H", [(1, 8), (5, 72), (3, 136), (700, 1000), (2, 4104), (2, 32760)])
+def test_residual_norm_in_bf16_alone_takes_multiples_of_8(pm, T, H):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H)
+    r, y = (torch.randn(T, H, generator=g, device="cuda") for _ in range(2))
+    gain = 1 + 0.2 * torch.randn(H, generator=g, device="cuda")
+    want = r + y
+    x = torch.full((T + 1, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    pm.residual_norm_q8(r, y, gain, 1e-6, T, H, None, None, x)
+    torch.cuda.synchronize()
+    assert torch.equal(r, want) and bool((x[T] == 7.0).all())
+    v, dv = norm_formula(want, gain, 1e-6)
+    check_near(x[:T], v, dv, 2.0 ** -8)
+
+
+def test_a_bf16_layer_of_a_width_of_8s(pm):
+    """DenseExperts takes bf16 matrices in multiples of 8, and so does every step of their layer."""
+    from bitplane_mixed_precision_b200.prompt import DenseExperts, PromptLayer
+    E, H, I, k, T = 5, 136, 72, 2, 30
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    X = DenseExperts(E, H, I, lambda e, m, w: w.copy_(0.1 * torch.randn(w.numel(), generator=g, device="cuda")), pm.BF16)
+    L = PromptLayer(X, k, T)
+    r = torch.randn(T, H, generator=g, device="cuda")
+    L.norm(r, None, T, eps=1e-6)
+    L.route(torch.randn(T, E, generator=g, device="cuda"), T)
+    y = L.forward(T)
+    torch.cuda.synchronize()
+    check_near(L.x[:T], *norm_formula(r, torch.ones(H, device="cuda"), 1e-6), 2.0 ** -8)
+    want = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    x, up, down = L.x.double(), X.up.double(), X.down.double()
+    for t in range(T):
+        for i in range(k):
+            e = int(L.ids[t, i])
+            p = up[e] @ x[t]
+            want[t] += float(L.w[t, i]) * (down[e] @ (p[:I] * torch.sigmoid(p[:I]) * p[I:]).bfloat16().double())
+    # two roundings to bf16 on the way (h, nearly always the same one, and the rows): 2^-8 each of what they carry
+    assert float((y - want).norm() / want.norm()) <= 2.0 ** -7

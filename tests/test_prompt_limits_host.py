@@ -34,3 +34,15 @@ def test_rows_whose_last_tile_would_leave_an_int(pm, gather):
     assert code(pm, 2 ** 31 - 1, 1, 8, gather) == 7
     assert code(pm, 2 ** 31 - 128, 1, 8, gather) == 7
     assert code(pm, 2 ** 31 - 129, 1, 8, gather) in (1, 2)
+
+
+def test_widths_of_the_norm(pm):
+    """Rows of 8-bit codes come in 128 columns; bf16 rows alone in 8, as bf16 matrices take them."""
+    for H, outs, want in ((136, (A, A, A), 1), (136, (A, A, None), 1), (132, (None, None, A), 1), (4, (None, None, A), 1),
+                          (136, (None, None, A), None), (8, (None, None, A), None)):
+        if want is None:
+            pm.residual_norm_q8(A, A, A, 0.0, 0, H, *outs)  # no rows: nothing to do
+        else:
+            with pytest.raises(pm.PmoeError) as ei:
+                pm.residual_norm_q8(A, A, A, 0.0, 0, H, *outs)
+            assert ei.value.code == want
