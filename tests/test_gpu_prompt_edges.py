@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from prompt_common import U, check_near, check_q8, offsets_of, quantize
+from prompt_common import U, check_near, check_q8, offsets_of, products, quantize, value_of
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +200,35 @@ def test_a_bf16_layer_of_a_width_of_8s(pm):
             want[t] += float(L.w[t, i]) * (down[e] @ (p[:I] * torch.sigmoid(p[:I]) * p[I:]).bfloat16().double())
     # two roundings to bf16 on the way (h, nearly always the same one, and the rows): 2^-8 each of what they carry
     assert float((y - want).norm() / want.norm()) <= 2.0 ** -7
+
+
+# ---------------------------------------------------------------- products
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("K,N", [(256, 1096), (1152, 776), (640, 2048)])
+def test_down_products_of_many_ragged_experts(pm, kind, out, K, N):
+    """Rows in place (no index), enough row tiles for 256 matrix rows a tile and several tiles for every SM: boxes of 32
+    and of 128 rows in turn, ragged last columns, rows behind the last expert left alone."""
+    rng = np.random.default_rng(K + N)
+    counts = [int(n) for n in rng.integers(0, 260, 90)]
+    counts[0], counts[7], counts[20], counts[50], counts[89] = 1, 0, 128, 1025, 64
+    M, extra = sum(counts), 5
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K)
+    x = torch.randn(M + extra, K, generator=g, device="cuda") * torch.exp(torch.randn(M + extra, 1, generator=g,
+                                                                                      device="cuda"))
+    w = torch.randn(len(counts), N, K, generator=g, device="cuda") * K ** -0.5
+    t, xs, ws = pm.BF16, None, None
+    if kind == "q8":
+        t, (x, xs), (w, ws) = pm.Q8, quantize(x), quantize(w)
+        x64, w64 = value_of(x, xs)[:M], value_of(w, ws)
+    else:
+        x, w = x.bfloat16(), w.bfloat16()
+        x64, w64 = x.double()[:M], w.double()
+    o = torch.full((M + extra, N), 7.0, dtype=torch.float32 if out == "f32" else torch.bfloat16, device="cuda")
+    pm.grouped_matmul(pm.make_dense(t, w, ws, len(counts), N, K), pm.make_rows(t, x, xs, M + extra), offsets_of(counts),
+                      M + extra, pm.F32 if out == "f32" else pm.BF16, o)
+    torch.cuda.synchronize()
+    check_near(o[:M], *products(x64, w64, counts), U if out == "f32" else 2.0 ** -8)
+    assert bool((o[M:] == 7.0).all())

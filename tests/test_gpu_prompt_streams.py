@@ -315,3 +315,39 @@ def test_a_layer_again_and_again_in_the_same_buffers(pm, kind, T):
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(run(False), want))
     assert float(want[0].abs().max()) < float("inf") and pm.grouped_error() == (0, 0)
+
+
+def test_a_captured_layer_behind_copies_and_a_join(pm):
+    """In a graph the launch in front may be a copy, or two branches that join: the early launch waits for those too."""
+    E, H, I, k, T = 9, 256, 128, 2, 200
+    X = experts(1, E, H, I, 11)
+    L, alone = PromptLayer(X, k, T), PromptLayer(X, k, T)
+    given = inputs(E, H, T, 12)
+    r, y, logits = (torch.zeros_like(a) for a in given)
+    staged = [a.clone() for a in given]
+    side = torch.cuda.Stream()
+    out = torch.empty(T, H, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000)
+            logits.copy_(staged[2])
+        r.copy_(staged[0])
+        y.copy_(staged[1])
+        L.norm(r, y, T)
+        main.wait_stream(side)
+        L.route(logits, T)
+        out.copy_(L.forward(T))
+    for seed in (13, 14, 15):
+        for to, a in zip(staged, inputs(E, H, T, seed)):
+            to.copy_(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        alone.norm(staged[0].clone(), staged[1], T)
+        alone.route(staged[2], T)
+        want = alone.forward(T)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
