@@ -23,13 +23,6 @@ __host__ __device__ __forceinline__ uint32_t scale_byte(uint32_t top)
 // 2^-e for a scale byte of a finite block (0..247): exact, never subnormal.
 __device__ __forceinline__ float inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// 2^e (2^-127, byte 0, is a subnormal float; byte 255 stands for NaN).
-__device__ __forceinline__ float value(uint32_t byte)
-{
-    return byte == 0u ? __uint_as_float(0x00400000u)
-                      : byte == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(byte << 23);
-}
-
 // Four values of one block to codes (rounded to nearest even: e4m3 has 3 mantissa bits, an error of at
 // most 2^-4 of the value). NaN blocks get the code of NaN throughout.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, uint32_t byte)

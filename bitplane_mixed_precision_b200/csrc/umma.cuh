@@ -221,8 +221,6 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint6
 // Scale words of 128 rows for the tensor cores: row r at byte (r % 32) * 16 + (r / 32) * 4 of a 512-byte
 // block, copied to four columns of tensor memory (repeated in each quarter of its lanes). MMAs that the same
 // thread issues later see it.
-__host__ __device__ constexpr uint32_t scale_offset(int r) { return (uint32_t)((r % 32) * 16 + (r / 32) * 4); }
-
 __device__ __forceinline__ void copy_scales(uint32_t taddr, const void *p)
 {
     const uint32_t a = pipe::smem_u32(p);
