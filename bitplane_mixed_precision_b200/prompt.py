@@ -15,8 +15,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (BF16, Q8, combine_rows, extract_prefix, group_pairs, group_workspace_bytes, grouped_matmul, grouped_swiglu,
-               make_dense, make_rows, quantize_q8, residual_norm_q8, route)
+from . import (BF16, Q8, _dense_ptr, combine_rows, extract_prefix, group_pairs, group_workspace_bytes, grouped_matmul,
+               grouped_swiglu, make_dense, make_rows, quantize_q8, residual_norm_q8, route)
 from .store import DOWN, GATE, UP, ResidentLayer
 
 
@@ -116,7 +116,7 @@ class PromptLayer:
     def route(self, logits, T: int, stream=None) -> None:
         """Experts and weights of the first T tokens from their router logits [T, E]."""
         self._tokens(T)
-        route(logits, T, self.experts.E, self.k, self.ids, self.w, self._stream(stream))
+        route(_dense_ptr(logits), T, self.experts.E, self.k, self.ids, self.w, self._stream(stream))
 
     def forward(self, T: int, stream=None) -> torch.Tensor:
         """The layer's output [T, H] for the first T rows of x, ids and w (an id outside 0..E-1 marks a

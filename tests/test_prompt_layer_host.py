@@ -103,3 +103,16 @@ def test_a_record_that_is_not_aligned_is_refused():
     with pytest.raises(pm.PmoeError) as ei:
         pm.grouped_matmul(pm.make_dense(1, A, A, 4, 64, 256), pm.make_rows(1, A, A, 10, None, A + 4), A, 10, 2, A)
     assert ei.value.code == 1
+
+
+def test_logits_with_gaps_are_refused(calls, monkeypatch):
+    """The router reads rows of E values one after another: columns of a wider tensor would be read as other tokens'."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    L = layer(0)
+    wide = torch.zeros(5, 8)
+    with pytest.raises(ValueError):
+        L.route(wide[:, :4], 5)
+    assert not calls
+    logits = wide[:, :4].contiguous()
+    L.route(logits, 5)
+    assert calls[0][1][0] == logits.data_ptr()
