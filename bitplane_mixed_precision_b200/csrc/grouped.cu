@@ -113,7 +113,7 @@ struct Bars {
     uint32_t tmem;
     int abort;
     int part[kThreads / 32];
-    // stages that a role has arrived for when it finishes (kNone owed where it has no part)
+    // stages that a role had arrived for when it gave up (kNone: it did not, or has no part)
     int64_t full_by[4];               // producer, scale warps, hand-over
     int64_t gathered_by[kGatherWarps];
 };
@@ -185,7 +185,7 @@ __device__ void drain(uint64_t *bar, uint32_t parity)
 // that stage). No owner is a whole turn of the ring ahead of another, so a barrier is at the phase of the last stage of
 // `end` that it belongs to, or behind it.
 template <int STAGES>
-__device__ void land(uint64_t *bars, int64_t end, const int64_t *stopped, int owners, uint32_t each, uint64_t deadline)
+__device__ __noinline__ void land(uint64_t *bars, int64_t end, const int64_t *stopped, int owners, uint32_t each, uint64_t deadline)
 {
     for (int64_t n = end > STAGES ? end - STAGES : 0; n < end; ++n) {
         uint64_t *bar = bars + n % STAGES;
@@ -206,8 +206,9 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Stages of this CTA's tiles t0, t0 + step, ... before tile t.
-__device__ __forceinline__ int64_t stages_before(const Grouped &g, int t, int t0, int step)
+// Stages of this CTA's tiles t0, t0 + step, ... before tile t. (Out of line, like land(): inside the roles' loops these
+// two, which no call needs that ends well, cost 0.5 of 16.3 us of a one-round product and 2 of 78 us of a q8 SwiGLU.)
+__device__ __noinline__ int64_t stages_before(const Grouped &g, int t, int t0, int step)
 {
     return (int64_t)((t - t0) / step) * g.iters;
 }
@@ -355,11 +356,10 @@ __device__ __forceinline__ bool epilogue_all(bool ok)
 // loaded together, while those of the four before are handed over. (Two or three such groups ahead, or a loop
 // unrolled over them, were 1 to 8 % slower.) rows_of(T, j) is the row's scale bytes, or NULL where
 // the values are zeros or not used (scale 1, so that zeros stay zeros).
-// Returns the stages it arrived for.
 template <class S, int ROWS, class RowsOf, class Tiles>
-__device__ __forceinline__ int64_t scale_warp(const Grouped &g, Bars *bars, const Waiter &wait, uint8_t *dst,
-                                              int tiles, int t0, int step, int where, const RowsOf &rows_of,
-                                              Tiles tile)
+__device__ __forceinline__ void scale_warp(const Grouped &g, Bars *bars, const Waiter &wait, uint8_t *dst, int tiles,
+                                           int t0, int step, int where, int64_t *stopped, const RowsOf &rows_of,
+                                           Tiles tile)
 {
     const int lane = threadIdx.x & 31;
     const int groups = (g.iters + 3) / 4;
@@ -400,8 +400,7 @@ __device__ __forceinline__ int64_t scale_warp(const Grouped &g, Bars *bars, cons
     };
     load();
     Ring<S::kStages> ring;
-    int t = t0;
-    for (; t < tiles; t += step) {
+    for (int t = t0; t < tiles; t += step) {
         for (int k = 0; k < g.iters; k += 4) {
             uint4 now[ROWS];
 #pragma unroll
@@ -412,8 +411,11 @@ __device__ __forceinline__ int64_t scale_warp(const Grouped &g, Bars *bars, cons
             for (int q = 0; q < 4; ++q) {
                 if (k + q >= g.iters)
                     break;
-                if (!ring.free(wait, bars, where))
-                    return stages_before(g, t, t0, step) + k + q;
+                if (!ring.free(wait, bars, where)) {
+                    if (lane == 0)
+                        *stopped = stages_before(g, t, t0, step) + k + q;
+                    return;
+                }
                 auto word = [&](int j) {
                     return j >= ROWS ? kOnes : q == 0 ? now[j].x : q == 1 ? now[j].y : q == 2 ? now[j].z : now[j].w;
                 };
@@ -429,7 +431,6 @@ __device__ __forceinline__ int64_t scale_warp(const Grouped &g, Bars *bars, cons
             }
         }
     }
-    return stages_before(g, t, t0, step);
 }
 
 template <bool Q8IN, bool SWIGLU, int ROWS, int NT, int OUT>
@@ -461,6 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         pipe::mbar_init(&bars->done, 1);
         bars->abort = 0;
+        for (int i = 0; i < 4; ++i)
+            bars->full_by[i] = kNone;
+        for (int i = 0; i < kGatherWarps; ++i)
+            bars->gathered_by[i] = kNone;
         pipe::fence_barrier_init();
         if (!g.index)
             tma::prefetch_map(&xmap);
@@ -490,16 +495,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- producer
         const bool leader = elect_one();
         Ring<S::kStages> ring;
-        int t = t0, i = 0;
-        for (; t < tiles; t += step) {
+        for (int t = t0; t < tiles; t += step) {
             const Tile T = tile(t);
             const bool one = ROWS == 128 && T.rows > 64; // one box of 128 rows
             const int loads = g.index ? 0 : one ? 1 : (T.rows + 31) / 32;
             const uint32_t bytes = (uint32_t)(loads * (one ? 128 : 32) * kRowBytes + S::kB);
-            for (i = 0; i < g.iters; ++i, ring.next()) {
+            for (int i = 0; i < g.iters; ++i, ring.next()) {
                 const int s = ring.s;
-                if (!ring.free(wait, bars, 1))
+                if (!ring.free(wait, bars, 1)) {
+                    if (lane == 0)
+                        bars->full_by[0] = stages_before(g, t, t0, step) + i;
                     goto produced;
+                }
                 uint8_t *a = smem + s * (S::kA + S::kB), *b = a + S::kA;
                 const int x = i * (kRowBytes / kElem);
                 if (leader) {
@@ -513,11 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            i = 0;
         }
     produced:
-        if (lane == 0)
-            bars->full_by[0] = stages_before(g, t, t0, step) + i;
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA: the warp goes through the stages together, one lane issues
@@ -575,10 +579,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 2) {
         // ---- scale bytes of the rows of x
-        int64_t arrived = kNone;
         if (Q8IN)
-            arrived = scale_warp<S, ROWS / 32>(
-                g, bars, wait, smem + S::kScalesAt, tiles, t0, step, 6,
+            scale_warp<S, ROWS / 32>(
+                g, bars, wait, smem + S::kScalesAt, tiles, t0, step, 6, &bars->full_by[1],
                 [&](const Tile &T, int r) -> const uint8_t * {
                     if (r >= T.rows)
                         return nullptr;
@@ -586,44 +589,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return (uint32_t)i < (uint32_t)g.n ? g.xs + (int64_t)i * (g.K / 32) : nullptr;
                 },
                 tile);
-        if (lane == 0)
-            bars->full_by[1] = arrived;
         __syncwarp();
     } else if (warp == 3) {
         // ---- scale bytes of the matrix rows
-        int64_t arrived = kNone;
         if (Q8IN)
-            arrived = scale_warp<S, NT / 32>(
-                g, bars, wait, smem + S::kScalesAt + 512, tiles, t0, step, 7,
+            scale_warp<S, NT / 32>(
+                g, bars, wait, smem + S::kScalesAt + 512, tiles, t0, step, 7, &bars->full_by[2],
                 [&](const Tile &T, int r) -> const uint8_t * {
                     const bool up = SWIGLU && (r & 32);
                     const int c = T.col0 + (SWIGLU ? (r / 64) * 32 + (r & 31) : r);
                     return c < g.width ? g.ws + ((int64_t)T.e * g.N + c + (up ? g.width : 0)) * (g.K / 32) : nullptr;
                 },
                 tile);
-        if (lane == 0)
-            bars->full_by[2] = arrived;
         __syncwarp();
     } else if (warp == 8 + kGatherWarps) {
         // ---- hands gathered rows over: the copies land as other threads' writes, which the tensor cores see behind
         // this fence
-        int64_t n = kNone;
         if (g.index) {
             Ring<S::kStages> ring;
-            const int64_t all = t0 < tiles ? (int64_t)((tiles - t0 - 1) / step + 1) * g.iters : 0;
             const bool leader = elect_one();
-            for (n = 0; n < all; ++n, ring.next()) {
-                if (!warp_wait(wait, &bars->gathered[ring.s], ring.phase, 11))
-                    break;
-                if (leader) {
-                    umma::fence_smem_async();
-                    pipe::mbar_arrive(&bars->full[ring.s]);
+            for (int t = t0; t < tiles; t += step)
+                for (int i = 0; i < g.iters; ++i, ring.next()) {
+                    if (!warp_wait(wait, &bars->gathered[ring.s], ring.phase, 11)) {
+                        if (lane == 0)
+                            bars->full_by[3] = stages_before(g, t, t0, step) + i;
+                        goto handed;
+                    }
+                    if (leader) {
+                        umma::fence_smem_async();
+                        pipe::mbar_arrive(&bars->full[ring.s]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-            }
         }
-        if (lane == 0)
-            bars->full_by[3] = n;
+    handed:
         __syncwarp();
     } else if (warp >= 8) {
         // ---- gathered rows of x: a thread has one 16-byte chunk of rows r0, r0 + 16, ...
@@ -632,8 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t pitch = (int64_t)g.K * kElem;
             const uint32_t at = (uint32_t)(r0 * kRowBytes + ((chunk ^ (r0 & 7)) << 4)); // 16 more rows: 2 KB more
             Ring<S::kStages> ring;
-            int t = t0, i = 0;
-            for (; t < tiles; t += step) {
+            for (int t = t0; t < tiles; t += step) {
                 const Tile T = tile(t);
                 const uint8_t *src[ROWS / 16];
                 uint32_t live = 0; // rows inside x
@@ -649,9 +647,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                for (i = 0; i < g.iters; ++i, ring.next()) {
-                    if (!ring.free(wait, bars, 9))
+                for (int i = 0; i < g.iters; ++i, ring.next()) {
+                    if (!ring.free(wait, bars, 9)) {
+                        if (lane == 0)
+                            bars->gathered_by[warp - 8] = stages_before(g, t, t0, step) + i;
                         goto gathered;
+                    }
                     const uint32_t dst = pipe::smem_u32(smem + ring.s * (S::kA + S::kB)) + at;
                     const uint32_t off = (uint32_t)i * kRowBytes;
                     const bool in = off + 16 * chunk < pitch;
@@ -663,12 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             copy16(dst + j * 16 * kRowBytes, src[j] + off, in && (live >> j & 1) ? 16 : 0);
                     copies_arrive(&bars->gathered[ring.s]);
                 }
-                i = 0;
             }
         gathered:
             asm volatile("cp.async.wait_all;" ::: "memory");
-            if (lane == 0)
-                bars->gathered_by[warp - 8] = stages_before(g, t, t0, step) + i;
             __syncwarp();
         }
     } else if (ROWS == 32) {
@@ -851,11 +849,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 0 && bars->abort) {
         const uint64_t deadline = pipe::globaltimer() + kDrainNs;
-        land<S::kStages>(bars->full, bars->full_by[0], bars->full_by, 4, 1, deadline);
+        const int64_t all = t0 < tiles ? stages_before(g, tiles - 1, t0, step) + g.iters : 0;
+        land<S::kStages>(bars->full, min(all, bars->full_by[0]), bars->full_by, 4, 1, deadline);
         if (g.index) {
             int64_t end = 0;
             for (int i = 0; i < kGatherWarps; ++i)
-                end = max(end, bars->gathered_by[i]);
+                end = max(end, min(all, bars->gathered_by[i]));
             land<S::kStages>(bars->gathered, end, bars->gathered_by, kGatherWarps, 32, deadline);
         }
     }
