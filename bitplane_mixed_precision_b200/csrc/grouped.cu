@@ -474,6 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
         umma::tmem_alloc(&bars->tmem, S::kTmemCols);
         umma::tmem_relinquish();
+        // only now: a launch behind this one that takes tensor memory early would keep it until this one has finished
+        pipe::launch_dependents();
     }
     // Zeros where no row of x will be: an MMA multiplies 128 rows whatever a tile has, and back to back these calls run
     // at the power limit, where zeros in place of what happened to lie there gain 1 to 4 %.
@@ -481,7 +483,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4 *>(smem + i / (S::kA / 16) * (S::kA + S::kB) + i % (S::kA / 16) * 16) =
             make_uint4(0, 0, 0, 0);
     umma::fence_smem_async();
-    pipe::launch_dependents();
     pipe::wait_prerequisites(); // nothing of another launch is read or written before this
     umma::fence_before_sync();
     row_tiles<ROWS>(g, first, bars->part); // ends with the block's barrier
