@@ -20,12 +20,22 @@ from . import (BF16, Q8, _dense_ptr, combine_rows, extract_prefix, group_pairs, 
 from .store import DOWN, GATE, UP, ResidentLayer
 
 
+def _floats(name, t, n: int) -> None:
+    """Refuses a tensor that is not float32 or has fewer than n elements: the library takes addresses and would read
+    past its end (None, and addresses as ints, pass)."""
+    if hasattr(t, "dtype") and (t.dtype != torch.float32 or t.numel() < n):
+        raise ValueError(f"{name}: float32 with at least {n} elements, not {t.dtype} with {t.numel()}")
+
+
 class DenseExperts:
     """The experts of one layer: [E][gate rows | up rows][H] and [E][H][I] in q8 or bf16."""
 
     def __init__(self, E: int, H: int, I: int, fill, kind: int = Q8, device="cuda", stream=None):
         """fill(expert, mat, w) writes float32 weights of shape (rows*cols,) into device tensor w
         (gate/up: I x H, down: H x I), on the current stream. H and I: multiples of 128 (q8) or 8 (bf16)."""
+        step = {Q8: 128, BF16: 8}.get(kind)
+        if step is None or not 1 <= E <= 2048 or min(H, I) < 1 or H % step or I % step:
+            raise ValueError(f"{E} experts of {H} x {I} in type {kind}: 1..2048 of multiples of 128 (q8) or 8 (bf16)")
         self.E, self.H, self.I, self.kind = E, H, I, kind
         dev = torch.device(device)
         st = stream if stream is not None else torch.cuda.current_stream(dev)
@@ -105,8 +115,12 @@ class PromptLayer:
         return stream if stream is not None else torch.cuda.current_stream(self.y.device)
 
     def norm(self, r, y, T: int, gain=None, eps: float = 0.0, stream=None) -> None:
-        """The layer's input from the residual stream: r += y (y may be None), x = r / rms(r) * gain."""
+        """The layer's input from the residual stream: r += y (y may be None), x = r / rms(r) * gain. All in float32:
+        r and y [T, H], gain [H]."""
         self._tokens(T)
+        H = self.experts.H
+        for name, t, n in (("r", r, T * H), ("y", y, T * H), ("gain", gain, H)):
+            _floats(name, t, n)
         x, stream = self.experts, self._stream(stream)
         if x.kind == Q8:
             residual_norm_q8(r, y, gain, eps, T, x.H, self.x, self.x_scales, None, stream)
@@ -114,8 +128,9 @@ class PromptLayer:
             residual_norm_q8(r, y, gain, eps, T, x.H, None, None, self.x, stream)
 
     def route(self, logits, T: int, stream=None) -> None:
-        """Experts and weights of the first T tokens from their router logits [T, E]."""
+        """Experts and weights of the first T tokens from their router logits, float32 [T, E]."""
         self._tokens(T)
+        _floats("logits", logits, T * self.experts.E)
         route(_dense_ptr(logits), T, self.experts.E, self.k, self.ids, self.w, self._stream(stream))
 
     def forward(self, T: int, stream=None) -> torch.Tensor:

@@ -116,3 +116,31 @@ def test_logits_with_gaps_are_refused(calls, monkeypatch):
     logits = wide[:, :4].contiguous()
     L.route(logits, 5)
     assert calls[0][1][0] == logits.data_ptr()
+
+
+def test_tensors_that_are_too_short_or_of_another_type_are_refused(calls, monkeypatch):
+    """The library takes addresses: a bf16 residual stream, or fewer rows than tokens, would be read past its end."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    L = layer(1)
+    r, y, gain, logits = torch.zeros(5, 256), torch.zeros(5, 256), torch.zeros(256), torch.zeros(5, 4)
+    for bad in (dict(r=r.bfloat16()), dict(r=r[:4]), dict(y=y.half()), dict(y=y[:4]), dict(gain=gain.double()),
+                dict(gain=gain[:255])):
+        with pytest.raises(ValueError):
+            L.norm(bad.get("r", r), bad.get("y", y), 5, bad.get("gain", gain))
+    for bad in (logits.bfloat16(), logits[:4], logits.long()):
+        with pytest.raises(ValueError):
+            L.route(bad, 5)
+    assert not calls
+    L.norm(r, None, 5)
+    L.norm(r.data_ptr(), y, 4, gain)
+    L.route(logits, 5)
+    assert len(calls) == 3
+
+
+@pytest.mark.parametrize("kind,E,H,I", [(1, 4, 192, 128), (1, 4, 128, 64), (0, 4, 132, 64), (0, 4, 64, 12), (2, 4, 128, 128),
+                                        (0, 0, 64, 64), (1, 2049, 128, 128), (1, 4, 0, 128)])
+def test_experts_that_no_product_would_take_are_refused(kind, E, H, I):
+    """Before they are filled: every product would refuse them, after minutes of filling."""
+    from bitplane_mixed_precision_b200.prompt import DenseExperts
+    with pytest.raises(ValueError):
+        DenseExperts(E, H, I, lambda e, m, w: None, kind, device="cpu")
