@@ -10,9 +10,9 @@
 // An SM takes in about 64 bytes per cycle: 48 KB take longer than the stage's MMAs (768 against 512 cycles at least),
 // which is what bounds long prompts. (Pairs of SMs sharing 256 x 256 tiles, 32 KB per SM and stage, gained 6 to 8 %
 // where experts have multiples of 256 rows and nothing on average over ragged ones.)
-// Measured: 16 experts of 1024 rows, 2048 x 4096: bf16 217 us (1265 TFLOP/s), q8 122 us (2244), with gathered rows 224
-// and 131 us; 300 experts of 40 rows, 4096 x 1024: 404 and 215 us (6.2 and 6.0 TB/s of weights); one token of ten
-// experts, q8 gate, up and SwiGLU, 2 x 1024 x 4096: 21 us, of which the weights stream for 13 (6.6 TB/s).
+// Measured: 16 experts of 1024 rows, 2048 x 4096: bf16 219 us (1258 TFLOP/s), q8 124 us (2221), with gathered rows 223
+// and 131 us; 300 experts of 40 rows, 4096 x 1024: 404 and 214 us (6.2 and 6.1 TB/s of weights); one token of ten
+// experts, q8 gate, up and SwiGLU, 2 x 1024 x 4096: 21 us (bf16 37), of which the weights stream for 13 (6.6 TB/s).
 // A persistent CTA per SM takes tiles at a stride of all of them: every role finds a tile's expert in a prefix
 // table of row tiles that the CTA makes from `offsets` when it starts. Roles, one warp each unless said otherwise:
 //   - producer: tiled TMA loads of 128 bytes of k per row into a ring of stages: the matrix rows and rows of x that
@@ -185,7 +185,8 @@ __device__ void drain(uint64_t *bar, uint32_t parity)
 // that stage). No owner is a whole turn of the ring ahead of another, so a barrier is at the phase of the last stage of
 // `end` that it belongs to, or behind it.
 template <int STAGES>
-__device__ __noinline__ void land(uint64_t *bars, int64_t end, const int64_t *stopped, int owners, uint32_t each, uint64_t deadline)
+__device__ __noinline__ void land(uint64_t *bars, int64_t end, const int64_t *stopped, int owners, uint32_t each,
+                                  uint64_t deadline)
 {
     for (int64_t n = end > STAGES ? end - STAGES : 0; n < end; ++n) {
         uint64_t *bar = bars + n % STAGES;
@@ -193,7 +194,8 @@ __device__ __noinline__ void land(uint64_t *bars, int64_t end, const int64_t *st
         for (int i = 0; i < owners; ++i)
             owed += stopped[i] <= n ? each : 0;
         if (owed)
-            asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(pipe::smem_u32(bar)), "r"(owed)
+            asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(pipe::smem_u32(bar)),
+                         "r"(owed)
                          : "memory");
         while (!pipe::mbar_try_wait(bar, (uint32_t)(n / STAGES) & 1) && pipe::globaltimer() < deadline) {
         }
@@ -934,8 +936,11 @@ pmoe_status grouped(const pmoe_dense *W, const pmoe_rows *X, const int32_t *offs
 
     // Rows of x per tile by the rows an expert has on average: at 16, tiles of 32 against 128 took 181 against 176 us
     // (q8, 256 experts of 4096 x 1024), 177 against 187 (q8 SwiGLU), 333 against 339 (bf16); at 32, 227 against 182 and
-    // 386 against 352. Matrix rows per tile by whether 256 give half of the SMs a tile: one row for each of 9 experts,
-    // 2048 x 4096, 18.4 us with 128 against 19.5 (72 tiles), of 10 experts 29.0 against 21.6 (80 tiles).
+    // 386 against 352. The mean does not see crowded experts: 512 tokens of ten of 512 under a Zipf load (exponent 1.1,
+    // mean 10, one of 457) take 634 against 619 us (q8 SwiGLU) and 330 against 317 (q8, 4096 x 1024), 256 tokens 512
+    // against 510 and 265 against 262, 64 tokens 274 against 278. Matrix rows per tile by whether 256 give half of the
+    // SMs a tile: one row for each of 9 experts, 2048 x 4096, 18.4 us with 128 against 19.5 (72 tiles), of 10 experts
+    // 29.0 against 21.6 (80 tiles).
     const int hit = W->E < rows ? W->E : rows;
     const int tile_rows = rows <= 16 * (int64_t)hit ? 32 : 128;
     const int64_t most = (int64_t)rows / tile_rows + hit; // at most one ragged row tile per expert

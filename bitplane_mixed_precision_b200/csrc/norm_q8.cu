@@ -63,12 +63,13 @@ template <int V> __device__ __forceinline__ float squares(const float4 (&v)[V])
 
 // One block per token, V float4 of the row per thread, held in registers between the sum of squares and
 // the output: r and y are read once and r written once. 8 neighbouring lanes hold one 32-column block. Bound by memory:
-// 4096 x 4096 takes 38 us, 5.8 TB/s of the 13 bytes an element that have to move (with r and y passed through the L2
-// as streams, which leaves its room to the codes that the next call reads: 37.9 us against 38.8).
+// 4096 x 4096 takes 39.2 us, 5.6 TB/s of the 13 bytes an element that have to move (r and y pass through the L2 as
+// streams, which leaves its room to the codes that the next call reads: 0.9 us less; the branch for rows whose squares
+// leave the floats costs 0.5 us).
 template <int V>
 __global__ void __launch_bounds__(kMaxNormThreads)
-    residual_norm_q8_kernel(float *__restrict__ r, const float *y, const float *gain, float eps, int H, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
-                            uint16_t *__restrict__ x)
+    residual_norm_q8_kernel(float *__restrict__ r, const float *y, const float *gain, float eps, int H,
+                            uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, uint16_t *__restrict__ x)
 {
     __shared__ float part[32], sums[32];
     __shared__ uint32_t tops[32];
