@@ -22,8 +22,8 @@ from .store import DOWN, GATE, UP, ResidentLayer
 
 def _floats(name, t, n: int) -> None:
     """Refuses a tensor that is not float32 or has fewer than n elements: the library takes addresses and would read
-    past its end (None, and addresses as ints, pass)."""
-    if hasattr(t, "dtype") and (t.dtype != torch.float32 or t.numel() < n):
+    past its end (None, and what is no tensor, pass)."""
+    if isinstance(t, torch.Tensor) and (t.dtype != torch.float32 or t.numel() < n):
         raise ValueError(f"{name}: float32 with at least {n} elements, not {t.dtype} with {t.numel()}")
 
 
