@@ -196,7 +196,7 @@ def test_a_product_that_gives_up_ends_once_its_own_copies_have_landed(pm, short_
 
 @pytest.mark.parametrize("kind", ["bf16", "q8"])
 @pytest.mark.parametrize("gather", [False, True])
-@pytest.mark.parametrize("rows", [20, 700])
+@pytest.mark.parametrize("rows", [5, 20, 700])
 def test_products_that_give_up_at_different_places(pm, kind, gather, rows):
     """Limits from 1 ns to some 50 us stop the roles at different stages; calls follow one another at once on the same
     SMs, and the first call with the default limit is exact again."""
